@@ -91,6 +91,202 @@ typedef struct {
   int64_t batch;
 } ps_kv_cache;
 
+/* ------------------------------------------------------------------ rotary positions
+ * How a head is rotated: which dims form a pair, how many of them turn, and the angle per
+ * position of every pair.  The pair i < rotary_dim / 2 of a token at position p is turned by
+ * p * inv_freq[i] (formed and reduced in float64), and scaled by attn_factor:
+ *   PS_ROPE_HALF        pairs dims (i, i + rotary_dim / 2)
+ *   PS_ROPE_INTERLEAVED pairs dims (2i, 2i + 1)
+ * Dims >= rotary_dim pass unrotated and unscaled.  A program fills one per model, with
+ * ps_rope_init or by hand, and keeps it. */
+#define PS_ROPE_HALF 0
+#define PS_ROPE_INTERLEAVED 1
+
+typedef struct {
+  int32_t layout;      /* PS_ROPE_HALF or PS_ROPE_INTERLEAVED                          */
+  int32_t rotary_dim;  /* dims that turn: a multiple of 16 in [0, head_dim]; 0: none   */
+  float attn_factor;   /* > 0; multiplies cos and sin (1: a plain rotation)            */
+  int32_t reserved;    /* must be 0                                                    */
+  double inv_freq[64]; /* [rotary_dim / 2], each in [0, 1]                             */
+} ps_rope;
+
+/* Frequencies for contexts longer than the trained one, from the plain
+ * f_i = rope_theta^(-2i / rotary_dim), with a stretch `factor` s >= 1:
+ *   PS_ROPE_SCALE_NONE     f_i
+ *   PS_ROPE_SCALE_LINEAR   f_i / s (positions interpolated)
+ *   PS_ROPE_SCALE_BY_PARTS g f_i + (1 - g) f_i / s with g = (r_i - low) / (high - low) clamped
+ *                          to [0, 1] and r_i = original_len f_i / (2 pi), the turns of pair i
+ *                          over the trained length: slow pairs are stretched, fast ones kept
+ *   PS_ROPE_SCALE_YARN     the same blend (YaRN) with its ramp over the pair index: g falls
+ *                          from 1 at floor(i(high)) to 0 at ceil(i(low)), both clamped to
+ *                          [0, rotary_dim - 1], where i(r) = rotary_dim ln(original_len /
+ *                          (2 pi r)) / (2 ln rope_theta) is the index that makes r turns
+ * (base-changing scalings are a different rope_theta). */
+#define PS_ROPE_SCALE_NONE 0
+#define PS_ROPE_SCALE_LINEAR 1
+#define PS_ROPE_SCALE_BY_PARTS 2
+#define PS_ROPE_SCALE_YARN 3
+
+typedef struct {
+  int32_t kind;        /* PS_ROPE_SCALE_*                                              */
+  int32_t reserved;    /* must be 0                                                    */
+  double factor;       /* s >= 1 (LINEAR, BY_PARTS, YARN)                              */
+  double low, high;    /* turns, 0 < low < high (BY_PARTS, YARN)                       */
+  double original_len; /* trained positions, > 0 (BY_PARTS, YARN)                      */
+} ps_rope_scaling;
+
+/* Fills *rope (host only, no GPU needed) from params->rope_theta (>= 1; > 1 for YARN) and the
+ * scaling (NULL: none).  attn_factor as in ps_rope. */
+int ps_rope_init(ps_rope* rope, const ps_params* params, int32_t layout, int32_t rotary_dim,
+                 const ps_rope_scaling* scaling, float attn_factor);
+
+/* RMS norm of every query and key head before it is rotated: x rstd w with
+ * rstd = 1 / sqrt(mean(x^2) + eps) over the head's dims and a weight shared by all heads. */
+#define PS_TYPE_BF16 0
+#define PS_TYPE_FP32 1
+
+typedef struct {
+  const void* q_weight; /* device [head_dim]; NULL: queries are not normalised          */
+  const void* k_weight; /* device [head_dim]; NULL: keys are not normalised             */
+  int32_t weight_type;  /* PS_TYPE_BF16 or PS_TYPE_FP32 (both weights)                  */
+  float eps;            /* >= 0, finite                                                 */
+} ps_qk_norm;
+
+/* Norm and rotation of queries and keys in one pass, e.g. ahead of ps_masked_prefill_attn.
+ * Each output is rounded to bf16 once, after the rotation.
+ *   rope   : host; required.
+ *   norm   : host or NULL (no norm).
+ *   q, k   : device bf16; token t's heads are contiguous at q + t * q_stride (elements),
+ *            [Hq, D], and k + t * k_stride, [Hkv, D], so both may be slices of one packed
+ *            projection row.  Strides: multiples of 8, at least Hq * D / Hkv * D.  Either of
+ *            q and k may be NULL together with its output.
+ *   pos    : device int64 [n_tokens], each token's position, 0 <= pos < 2^31.  A token outside
+ *            that range (PS_DEV_BAD_POS below, PS_DEV_POS_RANGE above), e.g. padding marked
+ *            -1, gets rows of zeros.
+ *   q_out  : device bf16 [n_tokens, Hq, D]; may be q itself when q_stride == Hq * D.
+ *   k_out  : device bf16 [n_tokens, Hkv, D]; may be k itself when k_stride == Hkv * D.
+ * Outputs overlap inputs in no other way. */
+int ps_qk_norm_rope(const ps_params* params, const ps_rope* rope, const ps_qk_norm* norm,
+                    const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const int64_t* pos, int64_t n_tokens, void* q_out, void* k_out,
+                    int32_t* dev_status, ps_stream_t stream);
+
+/* Bytes of device workspace ps_qk_norm_rope_bwd needs for n_tokens (partial sums of the
+ * weights' gradients).  0 on invalid arguments. */
+size_t ps_qk_norm_rope_bwd_workspace_bytes(const ps_params* params, int64_t n_tokens);
+
+/* Backward of ps_qk_norm_rope.  With n = x rstd, g = the output's gradient turned back by the
+ * token's angles (times attn_factor):
+ *   dx = rstd (w g - n mean(w g n)), dw = sum over tokens and heads of g n;  no norm: dx = g.
+ *   q, k             : the forward's inputs.  An input that is not normalised is not read and
+ *                      may be NULL; its gradients are still computed.
+ *   dq_out, dk_out   : device bf16 [n_tokens, Hq, D] / [n_tokens, Hkv, D], gradients of the
+ *                      outputs.  Either may be NULL together with its dq / dk.
+ *   dq, dk           : device bf16, written; token t at dq + t * dq_stride / dk + t * dk_stride
+ *                      (strides as the forward's).  May be dq_out / dk_out themselves when the
+ *                      stride is Hq * D / Hkv * D.  Tokens with a position outside the
+ *                      forward's range get zeros and add nothing to the weights' gradients.
+ *   dq_weight, dk_weight : device fp32 [D], written (not accumulated), or NULL when not wanted;
+ *                      must be NULL where the forward had no weight or no input.
+ *   workspace, ws_bytes  : device scratch of at least ps_qk_norm_rope_bwd_workspace_bytes(),
+ *                      256-byte aligned; may be NULL when no weight gradient is wanted.
+ * Sums run in a fixed order: the same inputs give the same bits. */
+int ps_qk_norm_rope_bwd(const ps_params* params, const ps_rope* rope, const ps_qk_norm* norm,
+                        const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const int64_t* pos, int64_t n_tokens, const void* dq_out,
+                        const void* dk_out, void* dq, int64_t dq_stride, void* dk,
+                        int64_t dk_stride, float* dq_weight, float* dk_weight, void* workspace,
+                        size_t ws_bytes, int32_t* dev_status, ps_stream_t stream);
+
+/* ps_kv_append_rope with a head norm and any ps_rope, reading packed projection rows: keys
+ * are normalised, rotated at pos0[b] + t and stored, values stored as they are, queries
+ * normalised and rotated into q_out.  Where a token's row goes, and which tokens are skipped
+ * (their q_out rows are zeros), is as ps_kv_append_rope; in addition a position >= 2^31 is
+ * skipped (PS_DEV_POS_RANGE).
+ *   k_new, v_new : device bf16, token (b, t) at k_new + (b * T + t) * k_stride, [Hkv, D].
+ *   q            : device bf16, token (b, t) at q + (b * T + t) * q_stride, [Hq, D], or NULL
+ *                  together with q_out.
+ *   q_out        : device bf16 [batch, T, Hq, D]; may be q itself when q_stride == Hq * D.
+ * rope, norm and strides as ps_qk_norm_rope. */
+int ps_kv_append_norm_rope(const ps_params* params, const ps_rope* rope, const ps_qk_norm* norm,
+                           const ps_kv_cache* cache, const void* k_new, int64_t k_stride,
+                           const void* v_new, int64_t v_stride, const void* q, int64_t q_stride,
+                           void* q_out, const int64_t* pos0, int32_t T, int32_t* dev_status,
+                           ps_stream_t stream);
+
+/* The same into the paged store of ps_kv_append_rope_paged. */
+int ps_kv_append_norm_rope_paged(const ps_params* params, const ps_rope* rope,
+                                 const ps_qk_norm* norm, void* k_pool, void* v_pool,
+                                 int64_t n_blocks, const int32_t* block_table,
+                                 int32_t table_stride, int64_t batch, const void* k_new,
+                                 int64_t k_stride, const void* v_new, int64_t v_stride,
+                                 const void* q, int64_t q_stride, void* q_out,
+                                 const int64_t* pos0, int32_t T, int32_t* dev_status,
+                                 ps_stream_t stream);
+
+/* 4-bit store: 144 bytes per token and KV head where the bf16 store takes 512.
+ * A row of 128 dims is two groups of 64 (dims [64 g, 64 g + 64)); a group keeps a bf16 scale s
+ * and minimum m and 4-bit codes u in 0..15, and stands for m + s u:
+ *   m = the least value, s = (greatest - least) / 15 (fp32, rounded to bf16),
+ *   u = (x - m) / s rounded to nearest even and clamped (0 where s is 0),
+ * x being the bf16 row that the bf16 store would hold.  A group with an infinity or a NaN, or
+ * whose spread or scale overflows, stands for NaN throughout.
+ *   payload : 64 bytes, sixteen 32-bit words; word 2 b + g holds dims 64 g + 8 b + e
+ *             (e = 0..7), code e at bit 4 (e >> 1) + 16 (e & 1).
+ *   record  : eight bf16 per row: K's s and m of group 0, of group 1, then V's.
+ * Layouts (device, 16-byte aligned, contiguous), with the rows of ps_kv_cache:
+ *   k_prefix, v_prefix : uint8 [batch, Hkv, l_prefix, 64];  s_prefix : bf16 [batch, Hkv, l_prefix, 8]
+ *   k_ring, v_ring     : uint8 [batch, Hkv, W, 64];         s_ring   : bf16 [batch, Hkv, W, 8]
+ * Prefix pointers may be NULL when l_prefix == 0.  Linear: ring pointers NULL, l_prefix = Lmax
+ * (every position must be < Lmax).
+ * Paged: block_table set (int32 [batch, table_stride], entries as ps_kv_append_rope_paged);
+ * then k_prefix, v_prefix are pools [n_blocks, Hkv, 64, 64] and s_prefix [n_blocks, Hkv, 64, 8],
+ * and the ring pointers are NULL.  Otherwise n_blocks and table_stride are 0. */
+typedef struct {
+  void* k_prefix;
+  void* v_prefix;
+  void* s_prefix;
+  void* k_ring;
+  void* v_ring;
+  void* s_ring;
+  int64_t batch;
+  const int32_t* block_table;
+  int64_t n_blocks;
+  int32_t table_stride;
+  int32_t reserved; /* must be 0 */
+} ps_kv_cache_q4;
+
+/* ps_kv_append_norm_rope into the 4-bit store: the same rows, quantised as they are written. */
+int ps_kv_append_norm_rope_q4(const ps_params* params, const ps_rope* rope,
+                              const ps_qk_norm* norm, const ps_kv_cache_q4* cache,
+                              const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                              const int64_t* pos0, int32_t T, int32_t* dev_status,
+                              ps_stream_t stream);
+
+/* Reads rows of the 4-bit store back as bf16, e.g. as the context of a later prefill: the
+ * values that the store's row of position pos0[b] + t stands for, rounded to bf16.  Which
+ * position a ring slot holds now is the caller's to know; of tokens that share a slot only the
+ * newest of the call is read.  The others, and positions the store has no row for (flagged as
+ * by the append), read as zeros.
+ *   k_out, v_out : device bf16 [batch, T, Hkv, D]; either may be NULL. */
+int ps_kv_read_q4(const ps_params* params, const ps_kv_cache_q4* cache, const int64_t* pos0,
+                  int32_t T, void* k_out, void* v_out, int32_t* dev_status, ps_stream_t stream);
+
+/* Bytes of device workspace ps_decode_attn_q4 needs for this geometry and batch (any store
+ * kind; for a linear store l_prefix = Lmax).  0 on invalid arguments. */
+size_t ps_decode_q4_workspace_bytes(const ps_params* params, int64_t batch);
+
+/* ps_decode_attn over the 4-bit store: attention of one query token per sequence over the
+ * values its visible rows stand for.  In a linear store (ring NULL) the query at pos[b] sees
+ * [0, pos[b]], and pos[b] >= l_prefix is skipped (PS_DEV_POS_RANGE).  Rows no visible position
+ * maps to may hold anything.  A block table entry outside [0, n_blocks) sets PS_DEV_POS_RANGE
+ * and that block's rows are left out.  Other arguments, results and errors as
+ * ps_decode_attn; the workspace is ps_decode_q4_workspace_bytes(), 16-byte aligned. */
+int ps_decode_attn_q4(const ps_params* params, const ps_kv_cache_q4* cache, const void* q,
+                      const int64_t* pos, void* out, float* lse, void* workspace,
+                      size_t ws_bytes, int32_t* dev_status, ps_stream_t stream);
+
 /* Append T tokens per sequence and apply Continue-PE RoPE exactly once.
  * Source: §位置编码 (Continue PE: absolute position ids, rotated K reused as cached),
  * §核心机制 (hard eviction, bounded per-sequence store).

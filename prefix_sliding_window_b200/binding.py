@@ -30,6 +30,15 @@ PS_DEV_TIMEOUT = 4
 PS_TILE_FULL = 1
 PS_TILE_PARTIAL = 2
 
+PS_ROPE_HALF = 0
+PS_ROPE_INTERLEAVED = 1
+PS_ROPE_SCALE_NONE = 0
+PS_ROPE_SCALE_LINEAR = 1
+PS_ROPE_SCALE_BY_PARTS = 2
+PS_ROPE_SCALE_YARN = 3
+PS_TYPE_BF16 = 0
+PS_TYPE_FP32 = 1
+
 
 class PsError(RuntimeError):
     def __init__(self, code: int, func: str, msg: str):
@@ -58,6 +67,52 @@ class PsKVCache(ctypes.Structure):
         ("k_ring", c_void_p),
         ("v_ring", c_void_p),
         ("batch", c_int64),
+    ]
+
+
+class PsRope(ctypes.Structure):
+    _fields_ = [
+        ("layout", c_int32),
+        ("rotary_dim", c_int32),
+        ("attn_factor", c_float),
+        ("reserved", c_int32),
+        ("inv_freq", c_double * 64),
+    ]
+
+
+class PsRopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", c_int32),
+        ("reserved", c_int32),
+        ("factor", c_double),
+        ("low", c_double),
+        ("high", c_double),
+        ("original_len", c_double),
+    ]
+
+
+class PsQkNorm(ctypes.Structure):
+    _fields_ = [
+        ("q_weight", c_void_p),
+        ("k_weight", c_void_p),
+        ("weight_type", c_int32),
+        ("eps", c_float),
+    ]
+
+
+class PsKVCacheQ4(ctypes.Structure):
+    _fields_ = [
+        ("k_prefix", c_void_p),
+        ("v_prefix", c_void_p),
+        ("s_prefix", c_void_p),
+        ("k_ring", c_void_p),
+        ("v_ring", c_void_p),
+        ("s_ring", c_void_p),
+        ("batch", c_int64),
+        ("block_table", c_void_p),
+        ("n_blocks", c_int64),
+        ("table_stride", c_int32),
+        ("reserved", c_int32),
     ]
 
 
@@ -112,6 +167,35 @@ _SIGS = {
                                              c_void_p, c_void_p]),
     "ps_decode_visible_ranges": (c_int32, [POINTER(PsParams), c_void_p, c_int64, c_void_p,
                                            c_void_p]),
+    "ps_rope_init": (c_int32, [POINTER(PsRope), POINTER(PsParams), c_int32, c_int32,
+                               POINTER(PsRopeScaling), c_float]),
+    "ps_qk_norm_rope": (c_int32, [POINTER(PsParams), POINTER(PsRope), POINTER(PsQkNorm), c_void_p,
+                                  c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_void_p, c_void_p, c_void_p]),
+    "ps_qk_norm_rope_bwd_workspace_bytes": (c_size_t, [POINTER(PsParams), c_int64]),
+    "ps_qk_norm_rope_bwd": (c_int32, [POINTER(PsParams), POINTER(PsRope), POINTER(PsQkNorm),
+                                      c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                      c_void_p]),
+    "ps_kv_append_norm_rope": (c_int32, [POINTER(PsParams), POINTER(PsRope), POINTER(PsQkNorm),
+                                         POINTER(PsKVCache), c_void_p, c_int64, c_void_p, c_int64,
+                                         c_void_p, c_int64, c_void_p, c_void_p, c_int32, c_void_p,
+                                         c_void_p]),
+    "ps_kv_append_norm_rope_paged": (c_int32, [POINTER(PsParams), POINTER(PsRope),
+                                               POINTER(PsQkNorm), c_void_p, c_void_p, c_int64,
+                                               c_void_p, c_int32, c_int64, c_void_p, c_int64,
+                                               c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                               c_void_p, c_int32, c_void_p, c_void_p]),
+    "ps_kv_append_norm_rope_q4": (c_int32, [POINTER(PsParams), POINTER(PsRope),
+                                            POINTER(PsQkNorm), POINTER(PsKVCacheQ4), c_void_p,
+                                            c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                            c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+    "ps_kv_read_q4": (c_int32, [POINTER(PsParams), POINTER(PsKVCacheQ4), c_void_p, c_int32,
+                                c_void_p, c_void_p, c_void_p, c_void_p]),
+    "ps_decode_q4_workspace_bytes": (c_size_t, [POINTER(PsParams), c_int64]),
+    "ps_decode_attn_q4": (c_int32, [POINTER(PsParams), POINTER(PsKVCacheQ4), c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "ps_check_wait_timeout": (c_int32, [c_void_p, c_void_p]),
     "ps_last_error": (c_char_p, []),
     "ps_version": (c_char_p, []),
@@ -173,6 +257,70 @@ def make_params(n_q_heads, n_kv_heads, head_dim=128, l_prefix=0, window=1, rope_
 
 def make_cache(k_prefix, v_prefix, k_ring, v_ring, batch: int) -> PsKVCache:
     return PsKVCache(_ptr(k_prefix), _ptr(v_prefix), _ptr(k_ring), _ptr(v_ring), int(batch))
+
+
+_ROPE_LAYOUTS = {"half": PS_ROPE_HALF, "interleaved": PS_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": PS_ROPE_SCALE_NONE, "linear": PS_ROPE_SCALE_LINEAR,
+                  "by_parts": PS_ROPE_SCALE_BY_PARTS, "yarn": PS_ROPE_SCALE_YARN}
+
+
+def make_rope(params: PsParams, layout="half", rotary_dim: int = 128, scaling="none", factor=1.0,
+              low=1.0, high=32.0, original_len=32768.0, attn_factor=1.0) -> PsRope:
+    """The rotary plan of a model (ps_rope_init); make it once and keep it."""
+    rope = PsRope()
+    sc = PsRopeScaling(_ROPE_SCALINGS[scaling], 0, float(factor), float(low), float(high),
+                       float(original_len))
+    rc = load().ps_rope_init(ctypes.byref(rope), ctypes.byref(params), _ROPE_LAYOUTS[layout],
+                             int(rotary_dim), ctypes.byref(sc), float(attn_factor))
+    _check(rc, "ps_rope_init")
+    return rope
+
+
+def make_norm(q_weight=None, k_weight=None, eps: float = 1e-6) -> PsQkNorm:
+    """Head norm of queries and keys: weights [128] on the GPU, both bf16 or both fp32 (None:
+    that side is not normalised)."""
+    import torch
+    types = {torch.bfloat16: PS_TYPE_BF16, torch.float32: PS_TYPE_FP32}
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    for w in given:
+        if not w.is_cuda or w.dtype not in types or w.shape != (128,) or not w.is_contiguous():
+            raise ValueError("norm weights are contiguous [128] CUDA tensors, bf16 or fp32")
+        if w.dtype != given[0].dtype or w.device != given[0].device:
+            raise ValueError("both norm weights have one type and one device")
+    norm = PsQkNorm(_ptr(q_weight), _ptr(k_weight),
+                    types[given[0].dtype] if given else PS_TYPE_BF16, float(eps))
+    norm.held = given  # the struct keeps only addresses
+    norm.device = given[0].device if given else None
+    return norm
+
+
+def make_cache_q4(prefix, ring, batch: int, block_table=None) -> PsKVCacheQ4:
+    """View of a 4-bit store.  prefix and ring: (k, v, record) tensors or None; paged: prefix
+    holds the pools, ring is None and block_table [batch, stride] int32 is given."""
+    import torch
+    held = [t for part in (prefix, ring) if part is not None for t in part]
+    for part in (prefix, ring):
+        for t, dtype, width in zip(part or (), (torch.uint8, torch.uint8, torch.bfloat16),
+                                   (64, 64, 8)):
+            if not t.is_cuda or t.dtype != dtype or t.shape[-1] != width or \
+                    t.shape[:-1] != part[0].shape[:-1] or not t.is_contiguous():
+                raise ValueError("a 4-bit store part is contiguous uint8 [..., 64] k and v and "
+                                 "bf16 [..., 8] records on the GPU")
+    n_blocks = stride = 0
+    if block_table is not None:
+        if not block_table.is_cuda or block_table.dtype != torch.int32 or \
+                block_table.dim() != 2 or not block_table.is_contiguous() or \
+                block_table.shape[0] < batch or prefix is None:
+            raise ValueError("block_table is a contiguous int32 [batch, stride] CUDA tensor "
+                             "beside the pools")
+        n_blocks, stride = int(prefix[0].shape[0]), int(block_table.shape[1])
+        held.append(block_table)
+    ptrs = [_ptr(t) if t is not None and t.numel() else None
+            for part in (prefix, ring) for t in (part or (None,) * 3)]
+    cache = PsKVCacheQ4(*ptrs, int(batch), _ptr(block_table), n_blocks, stride, 0)
+    cache.held = held  # the struct keeps only addresses
+    cache.device = held[0].device if held else None
+    return cache
 
 
 # ---------------------------------------------------------------- entry points
@@ -349,6 +497,201 @@ def ps_masked_prefill_attn_bwd(params: PsParams, q, k, v, out, dout, lse, batch:
                                            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), ws_bytes,
                                            _ptr(dev_status), _stream(stream))
     _check(rc, "ps_masked_prefill_attn_bwd")
+
+
+def _tensor(name: str, t, dtype, device, numel: int):
+    """A contiguous CUDA tensor of the library's type and of at least numel elements."""
+    if t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} of >= {numel} elements on {device} expected, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _heads(name: str, t, tokens: int, heads: int, device):
+    """Rows of heads: [tokens, heads, 128] (or leading dims that flatten to tokens) with heads
+    contiguous in a token.  Returns the address and the stride between tokens."""
+    import torch
+    sh, st = t.shape, t.stride()
+    ok = (t.dtype == torch.bfloat16 and t.device == device and len(sh) >= 3 and sh[-1] == 128
+          and sh[-2] == heads and st[-1] == 1 and (st[-2] == 128 or heads == 1))
+    n, stride = 1, heads * 128
+    if ok:
+        for size, step in zip(sh[-3::-1], st[-3::-1]):  # leading dims: evenly spaced tokens
+            if n == 1 and size != 1:
+                stride = step
+            ok = ok and (size == 1 or step == n * stride)
+            n *= size
+        ok = ok and n == tokens
+    if not ok:
+        raise ValueError(f"{name}: bf16 [{tokens}, {heads}, 128] with contiguous heads on {device} "
+                         f"expected, got {t.dtype} {tuple(sh)} strides {st} on {t.device}")
+    return t.data_ptr(), stride
+
+
+def _device_of(pos, norm=None, cache=None):
+    """The device of a call: the current one, where everything it is given lives."""
+    import torch
+    dev = pos.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"positions are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for what in (norm, cache):
+        if what is not None and getattr(what, "device", None) not in (None, dev):
+            raise ValueError(f"weights or cache on {what.device}, positions on {dev}")
+    return dev
+
+
+def _workspace(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _status_ptr(t, device):
+    import torch
+    return None if t is None else _tensor("dev_status", t, torch.int32, device, 1)
+
+
+def ps_qk_norm_rope(params: PsParams, rope: PsRope, norm, q, k, pos, q_out, k_out,
+                    dev_status=None, stream=None) -> None:
+    """Head norm (norm None: none) and rotation of q [N, Hq, 128] and k [N, Hkv, 128] (views of
+    packed rows allowed; either None with its output) at pos [N]."""
+    import torch
+    dev = _device_of(pos, norm)
+    n = pos.numel()
+    hq, hkv = params.n_q_heads, params.n_kv_heads
+    qp = kp = qo = ko = None
+    qs = ks = 0
+    if q is not None:
+        qp, qs = _heads("q", q, n, hq, dev)
+        qo = _tensor("q_out", q_out, torch.bfloat16, dev, n * hq * 128)
+    if k is not None:
+        kp, ks = _heads("k", k, n, hkv, dev)
+        ko = _tensor("k_out", k_out, torch.bfloat16, dev, n * hkv * 128)
+    rc = load().ps_qk_norm_rope(params, rope, norm, qp, qs, kp, ks,
+                                _tensor("pos", pos, torch.int64, dev, n), n, qo, ko,
+                                _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_qk_norm_rope")
+
+
+def ps_qk_norm_rope_bwd_workspace_bytes(params: PsParams, n_tokens: int) -> int:
+    return int(load().ps_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(params), int(n_tokens)))
+
+
+def ps_qk_norm_rope_bwd(params: PsParams, rope: PsRope, norm, q, k, pos, dq_out, dk_out, dq, dk,
+                        dq_weight=None, dk_weight=None, workspace=None, dev_status=None,
+                        stream=None) -> None:
+    """Gradients of ps_qk_norm_rope: dq, dk (views of packed rows allowed) and, where given, the
+    weights' (fp32 [128])."""
+    import torch
+    dev = _device_of(pos, norm)
+    n = pos.numel()
+    hq, hkv = params.n_q_heads, params.n_kv_heads
+    qp = kp = gq = gk = dqp = dkp = None
+    qs = ks = dqs = dks = 0
+    if q is not None:
+        qp, qs = _heads("q", q, n, hq, dev)
+    if k is not None:
+        kp, ks = _heads("k", k, n, hkv, dev)
+    if dq_out is not None:
+        gq = _tensor("dq_out", dq_out, torch.bfloat16, dev, n * hq * 128)
+        dqp, dqs = _heads("dq", dq, n, hq, dev)
+    if dk_out is not None:
+        gk = _tensor("dk_out", dk_out, torch.bfloat16, dev, n * hkv * 128)
+        dkp, dks = _heads("dk", dk, n, hkv, dev)
+    dwq = None if dq_weight is None else _tensor("dq_weight", dq_weight, torch.float32, dev, 128)
+    dwk = None if dk_weight is None else _tensor("dk_weight", dk_weight, torch.float32, dev, 128)
+    ws, ws_bytes = _workspace(workspace)
+    rc = load().ps_qk_norm_rope_bwd(params, rope, norm, qp, qs, kp, ks,
+                                    _tensor("pos", pos, torch.int64, dev, n), n, gq, gk, dqp, dqs,
+                                    dkp, dks, dwq, dwk, ws, ws_bytes,
+                                    _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_qk_norm_rope_bwd")
+
+
+def _append_rows(params, batch, k_new, v_new, q, q_out, pos0, T, dev):
+    import torch
+    n = int(batch) * int(T)
+    kp, ks = _heads("k_new", k_new, n, params.n_kv_heads, dev)
+    vp, vs = _heads("v_new", v_new, n, params.n_kv_heads, dev)
+    qp = qo = None
+    qs = 0
+    if q is not None:
+        qp, qs = _heads("q", q, n, params.n_q_heads, dev)
+        qo = _tensor("q_out", q_out, torch.bfloat16, dev, n * params.n_q_heads * 128)
+    return kp, ks, vp, vs, qp, qs, qo, _tensor("pos0", pos0, torch.int64, dev, batch), int(T)
+
+
+def ps_kv_append_norm_rope(params: PsParams, rope: PsRope, norm, cache: PsKVCache, k_new, v_new,
+                           q, q_out, pos0, T: int, dev_status=None, stream=None) -> None:
+    """ps_kv_append_rope with a head norm and any rotary plan; q (or None) goes to q_out."""
+    dev = _device_of(pos0, norm)
+    rc = load().ps_kv_append_norm_rope(params, rope, norm, cache,
+                                       *_append_rows(params, cache.batch, k_new, v_new, q, q_out,
+                                                     pos0, T, dev),
+                                       _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_kv_append_norm_rope")
+
+
+def ps_kv_append_norm_rope_paged(params: PsParams, rope: PsRope, norm, k_pool, v_pool,
+                                 block_table, batch: int, k_new, v_new, q, q_out, pos0, T: int,
+                                 dev_status=None, stream=None) -> None:
+    """The same into a paged store: pools [n_blocks, Hkv, 64, 128], block_table [batch, stride]."""
+    import torch
+    dev = _device_of(pos0, norm)
+    blocks = int(k_pool.shape[0])
+    rows = blocks * params.n_kv_heads * 64 * 128
+    rc = load().ps_kv_append_norm_rope_paged(
+        params, rope, norm, _tensor("k_pool", k_pool, torch.bfloat16, dev, rows),
+        _tensor("v_pool", v_pool, torch.bfloat16, dev, rows), blocks,
+        _tensor("block_table", block_table, torch.int32, dev, batch * block_table.shape[1]),
+        int(block_table.shape[1]), int(batch),
+        *_append_rows(params, batch, k_new, v_new, q, q_out, pos0, T, dev),
+        _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_kv_append_norm_rope_paged")
+
+
+def ps_kv_append_norm_rope_q4(params: PsParams, rope: PsRope, norm, cache: PsKVCacheQ4, k_new,
+                              v_new, q, q_out, pos0, T: int, dev_status=None,
+                              stream=None) -> None:
+    """The same into a 4-bit store (make_cache_q4)."""
+    dev = _device_of(pos0, norm, cache)
+    rc = load().ps_kv_append_norm_rope_q4(params, rope, norm, cache,
+                                          *_append_rows(params, cache.batch, k_new, v_new, q,
+                                                        q_out, pos0, T, dev),
+                                          _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_kv_append_norm_rope_q4")
+
+
+def ps_kv_read_q4(params: PsParams, cache: PsKVCacheQ4, pos0, T: int, k_out, v_out,
+                  dev_status=None, stream=None) -> None:
+    """Rows of positions [pos0, pos0 + T) of a 4-bit store as bf16 [batch, T, Hkv, 128]."""
+    import torch
+    dev = _device_of(pos0, None, cache)
+    n = cache.batch * int(T) * params.n_kv_heads * 128
+    out = [None if t is None else _tensor(name, t, torch.bfloat16, dev, n)
+           for name, t in (("k_out", k_out), ("v_out", v_out))]
+    rc = load().ps_kv_read_q4(params, cache, _tensor("pos0", pos0, torch.int64, dev, cache.batch),
+                              int(T), *out, _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_kv_read_q4")
+
+
+def ps_decode_q4_workspace_bytes(params: PsParams, batch: int) -> int:
+    return int(load().ps_decode_q4_workspace_bytes(ctypes.byref(params), int(batch)))
+
+
+def ps_decode_attn_q4(params: PsParams, cache: PsKVCacheQ4, q, pos, out, lse=None, workspace=None,
+                      dev_status=None, stream=None) -> None:
+    """ps_decode_attn over a 4-bit store."""
+    import torch
+    dev = _device_of(pos, None, cache)
+    rows = cache.batch * params.n_q_heads
+    ws, ws_bytes = _workspace(workspace)
+    rc = load().ps_decode_attn_q4(
+        params, cache, _tensor("q", q, torch.bfloat16, dev, rows * 128),
+        _tensor("pos", pos, torch.int64, dev, cache.batch),
+        _tensor("out", out, torch.bfloat16, dev, rows * 128),
+        None if lse is None else _tensor("lse", lse, torch.float32, dev, rows), ws, ws_bytes,
+        _status_ptr(dev_status, dev), _stream(stream))
+    _check(rc, "ps_decode_attn_q4")
 
 
 def ps_decode_visible_ranges(params: PsParams, pos, batch: int, ranges_out, stream=None) -> None:

@@ -7,6 +7,10 @@ eq. L_total).
 
 LinearCache: the full-attention comparator's cache [B, Hkv, Lmax, D], passed to the
 library as a prefix-only store with l_prefix = Lmax.
+
+QuantizedCache: the 4-bit store (144 bytes per token and KV head instead of 512): payloads
+[B, Hkv, rows, 64] uint8 of keys and of values and records [B, Hkv, rows, 8] bf16, for the
+prefix and the ring; window = 0 makes it linear (l_prefix = Lmax).
 """
 from __future__ import annotations
 
@@ -14,7 +18,7 @@ import math
 
 import torch
 
-from .binding import PsKVCache, make_cache, make_params
+from .binding import PsKVCache, PsKVCacheQ4, make_cache, make_cache_q4, make_params
 
 
 def _alloc(shape, device, fill):
@@ -62,6 +66,34 @@ class LinearCache:
     def params(self, n_q_heads: int, rope_theta: float = 1.0e6):
         """Parameters that make ps_kv_append_rope fill this linear cache."""
         return make_params(n_q_heads, self.n_kv_heads, self.head_dim, self.lmax, 1, rope_theta)
+
+
+class QuantizedCache:
+    def __init__(self, batch: int, n_kv_heads: int, l_prefix: int, window: int, device="cuda"):
+        self.batch, self.n_kv_heads = batch, n_kv_heads
+        self.l_prefix, self.window = l_prefix, window
+
+        def part(rows):
+            if rows == 0:
+                return None
+            shape = (batch, n_kv_heads, rows)
+            return (torch.zeros(*shape, 64, dtype=torch.uint8, device=device),
+                    torch.zeros(*shape, 64, dtype=torch.uint8, device=device),
+                    torch.zeros(*shape, 8, dtype=torch.bfloat16, device=device))
+
+        self.prefix, self.ring = part(l_prefix), part(window)
+        self._struct = make_cache_q4(self.prefix, self.ring, batch)
+
+    @property
+    def struct(self) -> PsKVCacheQ4:
+        return self._struct
+
+    def nbytes(self) -> int:
+        return self.batch * self.n_kv_heads * (self.l_prefix + self.window) * 144
+
+    def params(self, n_q_heads: int, rope_theta: float = 1.0e6):
+        return make_params(n_q_heads, self.n_kv_heads, 128, self.l_prefix, max(1, self.window),
+                           rope_theta)
 
 
 def default_scale(head_dim: int = 128) -> float:

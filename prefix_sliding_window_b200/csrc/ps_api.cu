@@ -21,7 +21,11 @@ namespace ps {
 
 namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
+void clear_error() { g_last_error.clear(); }
+
+namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -43,7 +47,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Validates the geometry shared by every call.
+}  // namespace
+
 int check_params(const ps_params* prm, bool need_window) {
   if (!prm) return fail(PS_ERR_INVALID_ARG, "params is NULL");
   if (prm->reserved != 0 || prm->reserved2 != 0)
@@ -70,7 +75,7 @@ float resolve_scale(const ps_params* prm) {
                                   : static_cast<float>(1.0 / sqrt(double(prm->head_dim)));
 }
 
-int check_ptr(const void* p, const char* name, bool nullable = false) {
+int check_ptr(const void* p, const char* name, bool nullable) {
   if (!p) {
     if (nullable) return PS_OK;
     return fail(PS_ERR_INVALID_ARG, std::string(name) + " is NULL");
@@ -78,14 +83,6 @@ int check_ptr(const void* p, const char* name, bool nullable = false) {
   if (!aligned16(p)) return fail(PS_ERR_INVALID_ARG, std::string(name) + " is not 16-byte aligned");
   return PS_OK;
 }
-
-#define PS_TRY(expr)             \
-  do {                           \
-    const int rc_ = (expr);      \
-    if (rc_ != PS_OK) return rc_; \
-  } while (0)
-
-}  // namespace
 
 int fail(int code, const std::string& msg) {
   g_last_error = msg;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,6 +20,21 @@ constexpr int kMaxGroup = 8;  // query heads per KV head handled by one decode C
 int fail(int code, const std::string& msg);
 // Maps a CUDA runtime error to PS_ERR_CUDA with its message (PS_OK if no error).
 int check_cuda(cudaError_t e, const char* what);
+
+// Forgets this thread's last failure message (every entry point starts with it).
+void clear_error();
+// Validates the geometry shared by every call.
+int check_params(const ps_params* prm, bool need_window);
+// The softmax scale: params->softmax_scale, or 1 / sqrt(head_dim) where that is 0.
+float resolve_scale(const ps_params* prm);
+// A device pointer: set (unless nullable) and 16-byte aligned.
+int check_ptr(const void* p, const char* name, bool nullable = false);
+
+#define PS_TRY(expr)             \
+  do {                           \
+    const int rc_ = (expr);      \
+    if (rc_ != PS_OK) return rc_; \
+  } while (0)
 
 // Encodes a 3-D bf16 tensor map [z][y][x] with a box of {box_x, box_y, 1} and 128-byte
 // swizzle.  Returns false (with a message recorded) on failure.
@@ -93,6 +109,108 @@ struct PinArgs {
   int32_t hkv, lp, w, lcap;
 };
 cudaError_t launch_pin(const PinArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norm + rotary positions
+// ps_rope as the kernels take it.
+struct RopeArgs {
+  int32_t interleaved;
+  int32_t dim;  // rotated dims
+  float attn;
+  double inv_freq[kHeadDim / 2];
+};
+struct NormArgs {
+  const void* wq;  // [D] or NULL: no norm
+  const void* wk;
+  int32_t fp32;    // the weights' type: fp32, else bf16
+  float eps;
+};
+struct NormRopeArgs {
+  const __nv_bfloat16* q;  // token t at q + t * q_stride, or NULL
+  const __nv_bfloat16* k;
+  int64_t q_stride, k_stride;
+  const int64_t* pos;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  int32_t* status;
+  int64_t n;
+  int32_t hq, hkv;
+  NormArgs norm;
+  RopeArgs rope;
+};
+struct NormRopeBwdArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  int64_t q_stride, k_stride;
+  const int64_t* pos;
+  const __nv_bfloat16* dq_out;  // NULL: no query side
+  const __nv_bfloat16* dk_out;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  int64_t dq_stride, dk_stride;
+  float* partial;  // [grid, 2 D] sums of the weights' gradients, or NULL
+  int32_t* status;
+  int64_t n;
+  int32_t hq, hkv;
+  NormArgs norm;
+  RopeArgs rope;
+};
+size_t norm_rope_bwd_workspace_bytes(int64_t n);
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+int launch_norm_rope_bwd(const NormRopeBwdArgs& a, float* dwq, float* dwk, cudaStream_t stream);
+
+// A store an append writes or a decode reads: prefix rows and ring slots of every (sequence, KV
+// head), contiguous or in 64-row blocks of one pool (then k[0], v[0], s[0] are the pools and
+// ring slots follow the prefix blocks in the table).  s: the records of a 4-bit store.
+struct StoreArgs {
+  uint8_t* k[2];  // [0] prefix, [1] ring
+  uint8_t* v[2];
+  uint8_t* s[2];
+  int32_t lp, w;
+  int32_t linear;  // no ring: positions are < lp
+  const int32_t* table;
+  int32_t table_stride, pre_blocks;
+  int64_t n_blocks;
+};
+struct AppendNormArgs {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* q;  // or NULL
+  int64_t k_stride, v_stride, q_stride;
+  __nv_bfloat16* q_out;
+  const int64_t* pos0;
+  int32_t* status;
+  int64_t batch;
+  int32_t T, hq, hkv;
+  StoreArgs store;
+  NormArgs norm;
+  RopeArgs rope;
+};
+int launch_append_norm(const AppendNormArgs& a, bool q4, cudaStream_t stream);
+struct ReadQ4Args {
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  const int64_t* pos0;
+  int32_t* status;
+  int64_t batch;
+  int32_t T, hkv;
+  StoreArgs store;
+};
+int launch_read_q4(const ReadQ4Args& a, cudaStream_t stream);
+
+struct DecodeQ4Launch {
+  const void* q;
+  const int64_t* pos;
+  void* out;
+  float* lse;
+  void* workspace;
+  int32_t* status;
+  int64_t batch;
+  int32_t hq, hkv;
+  float scale;
+  StoreArgs store;
+};
+size_t decode_q4_workspace_bytes(int64_t batch, int32_t hkv, int64_t max_keys);
+int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream);
 
 // ---------------------------------------------------------------- decode
 struct DecodeLaunch {
