@@ -6,10 +6,11 @@
 //   o_d = sum_k p_k m_kg + sum_k (p_k s_kg) u_kd,  p = softmax(scale S)
 // A row is 144 bytes (64 of K, 64 of V, 16 of scales and minima), so the kernel is bound by HBM
 // once the codes can be fed to the tensor cores cheaply:
-//  * a code u enters the matrix product as the bf16 number 128 + u, which is its four bits or-ed
-//    into 0x4300: one shift and one lop a pair, nothing rounded.  The 128s are taken off exactly:
-//    the score accumulators start at -128 sum q, and a product with a matrix of -128s sums the
-//    same rounded weights that the codes are multiplied by
+//  * a code u enters the matrix product as a bf16 subnormal: four bits at the bottom of a half
+//    word are u 2^-133 and the next four, masked in place, 16 u 2^-133 (exact: the exponent field
+//    stays 0 or 1, which share a spacing; the tensor cores take subnormals in full).  A word of
+//    eight codes costs one shift and four ands.  Queries and weights carry a factor 2^64 against
+//    the small codes, taken off with the 2^-133 and the 16s after the sums
 //  * the dims of a row are stored so that one 16-byte load gives a lane the words of a whole
 //    K fragment row; which dim goes to which position of the product does not matter as long as
 //    the query's fragment agrees
@@ -44,6 +45,9 @@ static_assert(kWarpBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fit
 constexpr int kMinRowsPerBlock = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLiftLog2 = 64.f;
+constexpr float kLift = 18446744073709551616.f;          // 2^64: queries and weights
+constexpr float kUncode = 590295810358705651712.f;       // 2^69 = 2^133 / 2^64
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
 constexpr float kMaxSlack = 8.f;
@@ -100,76 +104,84 @@ __device__ __forceinline__ RowScan scan_rows(const DecodeQ4Args& a, int lane, bo
   return s;
 }
 
-// Rows of one sequence that a warp's lane 0 copies, and where they are.
-struct Sequence {
-  int64_t p, n, pre;  // position, visible rows, visible prefix rows
+// The unit a block works on.
+struct Unit {
+  int64_t p;       // position
+  uint32_t n, pre; // visible rows, visible prefix rows
+  uint32_t slot0;  // ring slot of the oldest window row
   int32_t b, h;
 };
 
-// Copies visible rows [v, v + cnt) of a unit into a stage; returns (all lanes) the mask of rows
-// that are there (a bad block table entry leaves its rows out).  Lane 0 works.
-__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Sequence& sq, int64_t v,
-                                          int cnt, uint8_t* stage, uint64_t* bar,
-                                          uint32_t* mask) {
+__device__ __forceinline__ void enter(const DecodeQ4Args& a, Unit& u) {
+  u.pre = min(u.n, static_cast<uint32_t>(a.store.lp));
+  u.slot0 = u.n > u.pre ? static_cast<uint32_t>(mod_nonneg(
+                              u.p + 1 - (u.n - u.pre) - a.store.lp, a.store.w))
+                        : 0;
+}
+
+// What one of the three copying lanes (0: K, 1: V, 2: records) needs for a unit.
+struct Source {
+  const uint8_t* base[2];  // its unit's rows in the prefix and in the ring (or the pool)
+  uint32_t row_bytes;
+};
+
+__device__ __forceinline__ Source source_of(const DecodeQ4Args& a, const Unit& u, int lane) {
   const StoreArgs& st = a.store;
-  uint32_t tx = 0, there = 0;
-  for (int done = 0; done < cnt;) {
-    const int64_t x = v + done;
-    const bool ring = x >= sq.pre;
-    // prefix position x, or the window's (x - pre)-th oldest
-    const int64_t row = ring ? mod_nonneg(sq.p + 1 - (sq.n - x) - st.lp, st.w) : x;
-    int64_t run = cnt - done;
-    const int64_t left = ring ? st.w - row : sq.pre - x;
-    if (run > left) run = left;
-    int64_t at;  // row in its array
-    const int arr = (ring && !st.table) ? 1 : 0;
+  Source s;
+  s.row_bytes = lane == 2 ? kQ4RecordBytes : kQ4RowBytes;
+  const int64_t unit = (int64_t)u.b * a.hkv + u.h;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint8_t* b = lane == 0 ? st.k[i] : lane == 1 ? st.v[i] : st.s[i];
+    s.base[i] = st.table ? b : b + unit * (i ? st.w : st.lp) * s.row_bytes;
+  }
+  return s;
+}
+
+// Lanes 0..2 copy visible rows [x, x + cnt) of the unit into a stage; `mask` gets the rows that
+// are there (a bad block table entry leaves its rows out).
+__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, const Source& src,
+                                          int lane, uint32_t x, uint32_t cnt, uint8_t* stage,
+                                          uint64_t* bar, uint32_t* mask) {
+  const StoreArgs& st = a.store;
+  uint8_t* dst = stage + (lane == 2 ? 2 : lane) * kTile * kQ4RowBytes;
+  uint32_t copied = cnt, there = cnt == 32 ? 0xffffffffu : (1u << cnt) - 1u;
+  for (uint32_t done = 0; done < cnt;) {
+    // prefix position x, or the window's (x - pre)-th oldest row
+    const bool ring = x >= u.pre;
+    uint32_t row = ring ? u.slot0 + (x - u.pre) : x;
+    if (ring && row >= static_cast<uint32_t>(st.w)) row -= st.w;
+    uint32_t run = min(cnt - done, (ring ? st.w - row : u.pre - x));
+    const uint8_t* from = src.base[ring ? 1 : 0] + (int64_t)row * src.row_bytes;
     bool ok = true;
     if (st.table) {
-      const int64_t in_block = row & 63;
-      if (run > 64 - in_block) run = 64 - in_block;
+      run = min(run, 64 - (row & 63));
       const int32_t blk =
-          st.table[(int64_t)sq.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
+          st.table[(int64_t)u.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
       ok = blk >= 0 && blk < st.n_blocks;
-      at = ((int64_t)blk * a.hkv + sq.h) * 64 + in_block;
-    } else {
-      at = ((int64_t)sq.b * a.hkv + sq.h) * (ring ? st.w : st.lp) + row;
+      from = src.base[0] + (((int64_t)blk * a.hkv + u.h) * 64 + (row & 63)) * src.row_bytes;
     }
-    const uint32_t n = static_cast<uint32_t>(run);
     if (ok) {
-      bulk_load(stage + done * kQ4RowBytes, st.k[arr] + at * kQ4RowBytes, n * kQ4RowBytes, bar);
-      bulk_load(stage + (kTile + done) * kQ4RowBytes, st.v[arr] + at * kQ4RowBytes,
-                n * kQ4RowBytes, bar);
-      bulk_load(stage + 2 * kTile * kQ4RowBytes + done * kQ4RecordBytes,
-                st.s[arr] + at * kQ4RecordBytes, n * kQ4RecordBytes, bar);
-      tx += n * (2 * kQ4RowBytes + kQ4RecordBytes);
-      there |= (n == 32 ? 0xffffffffu : ((1u << n) - 1u)) << done;
-    } else if (a.status) {
-      atomicOr(a.status, PS_DEV_POS_RANGE);
+      bulk_load(dst + done * src.row_bytes, from, run * src.row_bytes, bar);
+    } else {
+      if (a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
+      there &= ~((run == 32 ? 0xffffffffu : (1u << run) - 1u) << done);
+      copied -= run;
     }
-    done += static_cast<int>(n);
+    done += run;
+    x += run;
   }
-  *mask = there;
-  mbar_arrive_expect_tx(bar, tx);
+  if (lane == 0) {
+    *mask = there;
+    // the phase cannot end before this arrival, whichever copies have landed by then
+    mbar_arrive_expect_tx(bar, copied * (2 * kQ4RowBytes + kQ4RecordBytes));
+  }
 }
 
-// D = A B + C
-__device__ __forceinline__ void mma_bf16_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1, float c0,
-                                           float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
-// Codes i (low half) and i + 4 (high half) of a word's eight as the bf16 pair 128 + u.
-template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w >> (4 * I)));
-  return r;
-}
+// Code pairs of a word as bf16 subnormals: codes 0 and 4 of its eight (low and high half), then
+// 1 and 5 (times 16); 2 and 6, 3 and 7 are the same of the word shifted down by 8.
+__device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -177,9 +189,8 @@ __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0
 // One warp's running softmax and accumulators over the heads (2 t, 2 t + 1) of its lane's t.
 struct State {
   float m[2], l[2];
-  float o[8][4];    // tile 4 g + i: dims 64 g + 8 (lane / 4) + 2 i + {0, 1}, heads 2 t + {0, 1}
-  float off[2][4];  // -128 sum of a group's weights (rows alike)
-  float mn[2][2];   // sum p m of a group, over this lane's rows
+  float o[8][4];   // tile 4 g + i: dims 64 g + 8 (lane / 4) + 2 i + {0, 1}, heads 2 t + {0, 1}
+  float mn[2][2];  // sum p m of a group, over this lane's rows
 };
 
 // The tile row of product row r (0..7): even rows first, so that the four rows a lane's V words
@@ -202,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
   pdl_trigger();
 
   // ------------------------------------------------ this block's share of the rows
-  Sequence sq;
-  int64_t off = 0, left;  // first row in the current unit, rows of the share still to do
+  Unit u;
+  uint32_t off = 0;  // first row in the current unit
+  int64_t left;      // rows of the share still to do
   if (a.ws_o) {
     const RowScan sc = scan_rows(a, lane, blockIdx.x == 0 && warp == 0);
     const int64_t total = sc.total * a.hkv;
@@ -215,64 +227,76 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
                                                         t0 < a.hkv * (sc.before + sc.mine));
     const int src = __ffs(has) - 1;
     int64_t rest = t0 - a.hkv * __shfl_sync(0xffffffffu, sc.before, src);
-    sq.b = src * sc.per;
+    u.b = src * sc.per;
+    int64_t n;
     while (true) {
-      sq.p = a.pos[sq.b];
-      sq.n = visible_rows(a, sq.p);
-      if (rest < a.hkv * sq.n) break;
-      rest -= a.hkv * sq.n;
-      ++sq.b;
+      u.p = a.pos[u.b];
+      n = visible_rows(a, u.p);
+      if (rest < a.hkv * n) break;
+      rest -= a.hkv * n;
+      ++u.b;
     }
-    sq.h = static_cast<int32_t>(div_nonneg(rest, sq.n));
-    off = rest - sq.h * sq.n;
+    u.n = static_cast<uint32_t>(n);
+    u.h = static_cast<int32_t>(div_nonneg(rest, n));
+    off = static_cast<uint32_t>(rest - u.h * n);
   } else {
-    sq.b = blockIdx.x / a.hkv;
-    sq.h = blockIdx.x % a.hkv;
-    sq.p = a.pos[sq.b];
-    sq.n = left = visible_rows(a, sq.p);
+    u.b = blockIdx.x / a.hkv;
+    u.h = blockIdx.x % a.hkv;
+    u.p = a.pos[u.b];
+    left = visible_rows(a, u.p);
+    u.n = static_cast<uint32_t>(left);
     if (left == 0 && threadIdx.x == 0 && a.status)
-      atomicOr(a.status, sq.p < 0 ? PS_DEV_BAD_POS : PS_DEV_POS_RANGE);
+      atomicOr(a.status, u.p < 0 ? PS_DEV_BAD_POS : PS_DEV_POS_RANGE);
   }
 
-  int issued = 0, used = 0;  // tiles of this warp so far: stage i % kStages, phase i / kStages
+  // scores come out of the products times 2^(64 - 133); c takes that off and scales to base 2
+  const float c = a.scale_log2 * kUncode;
+  int in = 0, at = 0;      // stage the next tile goes to, stage the next tile comes from
+  uint32_t phase = 0;      // of stage `at`
   while (true) {
-    sq.pre = sq.n < a.store.lp ? sq.n : a.store.lp;
-    const int64_t piece = left < sq.n - off ? left : sq.n - off;
+    enter(a, u);
+    const Source src = source_of(a, u, lane);
+    const uint32_t piece = static_cast<uint32_t>(left < u.n - off ? left : u.n - off);
     const int tiles = static_cast<int>((piece + kTile - 1) / kTile);
     const int my_tiles = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    auto issue = [&](int i) {  // this warp's i-th tile of the piece
-      if (lane == 0) {
-        const int64_t r = (int64_t)(warp + kWarps * i) * kTile;
-        const int cnt = static_cast<int>(piece - r < kTile ? piece - r : kTile);
-        const int s = issued % kStages;
-        load_tile(a, sq, off + r, cnt, mine + s * kStageBytes, &s_full[warp][s],
-                  &s_mask[warp][s]);
+    int issued = 0;
+    auto issue = [&]() {  // this warp's next tile of the piece
+      if (lane < 3) {
+        const uint32_t r = static_cast<uint32_t>(warp + kWarps * issued) * kTile;
+        load_tile(a, u, src, lane, off + r, min(piece - r, static_cast<uint32_t>(kTile)),
+                  mine + in * kStageBytes, &s_full[warp][in], &s_mask[warp][in]);
       }
+      in = in == kStages - 1 ? 0 : in + 1;
       ++issued;
     };
-    for (int i = 0; i < my_tiles && i < kStages; ++i) issue(i);
+    while (issued < my_tiles && issued < kStages) issue();
 
-    // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups
-    uint4 qf[2][2];
+    // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^64 (2^60
+    // where the codes come out 16 times as large); and each group's sum of query dims
+    uint32_t qf[2][2][4];
     float qs[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      qf[g][0] = qf[g][1] = make_uint4(0, 0, 0, 0);
-      if (g8 < a.group) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((int64_t)sq.b * a.hq + sq.h * a.group + g8) * kHeadDim + 64 * g + 16 * t4);
-        qf[g][0] = src[0];
-        qf[g][1] = src[1];
-      }
-      const uint32_t w[8] = {qf[g][0].x, qf[g][0].y, qf[g][0].z, qf[g][0].w,
-                             qf[g][1].x, qf[g][1].y, qf[g][1].z, qf[g][1].w};
-      float v = 0.f;
+      qs[g] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v += lo_f(w[i]) + hi_f(w[i]);
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
-      qs[g] = v + __shfl_xor_sync(0xffffffffu, v, 2);
+      for (int j = 0; j < 2; ++j) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (g8 < a.group)
+          w = *reinterpret_cast<const uint4*>(
+              a.q + ((int64_t)u.b * a.hq + u.h * a.group + g8) * kHeadDim + 64 * g + 16 * t4 +
+              8 * j);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = (i & 1) ? kLift / 16.f : kLift;
+          qs[g] += lo_f(ww[i]) + hi_f(ww[i]);
+          qf[g][j][i] = cvt_bf16x2(lo_f(ww[i]) * f, hi_f(ww[i]) * f);
+        }
+      }
+      qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
+      qs[g] = (qs[g] + __shfl_xor_sync(0xffffffffu, qs[g], 2)) * (1.f / kUncode);
     }
-    float Q[2][2];  // sum of a group's query dims, heads 2 t + e
+    float Q[2][2];  // of heads 2 t + e, on the products' scale
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -283,25 +307,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
     st.l[0] = st.l[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      st.off[g][0] = st.off[g][1] = st.off[g][2] = st.off[g][3] = 0.f;
-      st.mn[g][0] = st.mn[g][1] = 0.f;
-    }
+    st.mn[0][0] = st.mn[0][1] = st.mn[1][0] = st.mn[1][1] = 0.f;
+    // a score (before c) above this moves the running maximum
+    float above[2] = {-INFINITY, -INFINITY};
+    // weights are 2^(c x - m + 64): taken with -m + 64 in one step
+    float shift[2] = {kLiftLog2, kLiftLog2};
 
     const int kr = tile_row(g8);  // this lane's K rows: kr, kr + 8
     for (int i = 0; i < my_tiles; ++i) {
-      const int s = used % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[warp][s], (used / kStages) & 1, a.status))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[warp][at], phase, a.status))) {
         // given up on (and flagged): see the other copies in flight to their end as well
-        for (++used; used < issued; ++used)
-          mbar_wait(&s_full[warp][used % kStages], (used / kStages) & 1, a.status);
+        for (int j = i + 1; j < issued; ++j) {
+          if (++at == kStages) at = 0, phase ^= 1;
+          mbar_wait(&s_full[warp][at], phase, a.status);
+        }
+        if (++at == kStages) at = 0, phase ^= 1;
         break;
       }
-      ++used;
-      const uint8_t* stage = mine + s * kStageBytes;
+      const uint8_t* stage = mine + at * kStageBytes;
       const uint8_t* rec = stage + 2 * kTile * kQ4RowBytes;
-      const uint32_t mask = s_mask[warp][s];
+      const uint32_t mask = s_mask[warp][at];
+      if (++at == kStages) at = 0, phase ^= 1;
       // ---------------------------------------- scores of 2 x 16 rows
       float x[2][4];
 #pragma unroll
@@ -314,17 +340,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         float acc[2][4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float n0 = -128.f * Q[g][0], n1 = -128.f * Q[g][1];
-          const uint32_t a0 = g ? w0.y : w0.x, a1 = g ? w1.y : w1.x;
-          const uint32_t b0 = g ? w0.w : w0.z, b1 = g ? w1.w : w1.z;
-          mma_bf16_c(acc[g], code_pair<0>(a0), code_pair<0>(a1), code_pair<1>(a0),
-                     code_pair<1>(a1), qf[g][0].x, qf[g][0].y, n0, n1, n0, n1);
-          mma_bf16_16816(acc[g], code_pair<2>(a0), code_pair<2>(a1), code_pair<3>(a0),
-                         code_pair<3>(a1), qf[g][0].z, qf[g][0].w);
-          mma_bf16_16816(acc[g], code_pair<0>(b0), code_pair<0>(b1), code_pair<1>(b0),
-                         code_pair<1>(b1), qf[g][1].x, qf[g][1].y);
-          mma_bf16_16816(acc[g], code_pair<2>(b0), code_pair<2>(b1), code_pair<3>(b0),
-                         code_pair<3>(b1), qf[g][1].z, qf[g][1].w);
+          acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {  // words 2 j + g of the lane's four
+            const uint32_t a0 = j ? (g ? w0.w : w0.z) : (g ? w0.y : w0.x);
+            const uint32_t a1 = j ? (g ? w1.w : w1.z) : (g ? w1.y : w1.x);
+            const uint32_t b0 = a0 >> 8, b1 = a1 >> 8;
+            mma_bf16_16816(acc[g], pair_lo(a0), pair_lo(a1), pair_hi(a0), pair_hi(a1),
+                           qf[g][j][0], qf[g][j][1]);
+            mma_bf16_16816(acc[g], pair_lo(b0), pair_lo(b1), pair_hi(b0), pair_hi(b1),
+                           qf[g][j][2], qf[g][j][3]);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -333,10 +359,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
           s1 = fmaf(lo_f(c1.y), acc[1][2 + e], s1);
           s0 = fmaf(hi_f(c0.x), Q[0][e], s0);
           s1 = fmaf(hi_f(c1.x), Q[0][e], s1);
-          s0 = fmaf(hi_f(c0.y), Q[1][e], s0);
-          s1 = fmaf(hi_f(c1.y), Q[1][e], s1);
-          x[blk][e] = s0 * a.scale_log2;
-          x[blk][2 + e] = s1 * a.scale_log2;
+          x[blk][e] = fmaf(hi_f(c0.y), Q[1][e], s0);
+          x[blk][2 + e] = fmaf(hi_f(c1.y), Q[1][e], s1);
         }
       }
       if (mask != 0xffffffffu) {
@@ -349,36 +373,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       // ---------------------------------------- running maximum
       float mx[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-      }
-      if (__any_sync(0xffffffffu, mx[0] > st.m[0] + kMaxSlack || mx[1] > st.m[1] + kMaxSlack)) {
-        float c[2];
+      for (int e = 0; e < 2; ++e)
+        mx[e] = fmaxf(max3f(x[0][e], x[0][2 + e], x[1][e]), x[1][2 + e]);
+      if (__any_sync(0xffffffffu, mx[0] > above[0] || mx[1] > above[1])) {
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(st.m[e], mx[e]);
-          c[e] = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - mn);
-          st.m[e] = mn;
-          st.l[e] *= c[e];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            st.off[g][e] *= c[e];
-            st.off[g][2 + e] *= c[e];
-            st.mn[g][e] *= c[e];
+          for (int o = 4; o < 32; o <<= 1)
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+          const float m = fmaxf(st.m[e], mx[e] * c);
+          f[e] = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - m);
+          st.m[e] = m;
+          if (m != -INFINITY) {
+            shift[e] = kLiftLog2 - m;
+            above[e] = (m + kMaxSlack) / c;
           }
+          st.l[e] *= f[e];
+          st.mn[0][e] *= f[e];
+          st.mn[1][e] *= f[e];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          st.o[j][0] *= c[0];
-          st.o[j][1] *= c[1];
-          st.o[j][2] *= c[0];
-          st.o[j][3] *= c[1];
+          st.o[j][0] *= f[0];
+          st.o[j][1] *= f[1];
+          st.o[j][2] *= f[0];
+          st.o[j][3] *= f[1];
         }
       }
-      const float ref0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
-      const float ref1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
       // ---------------------------------------- weights and values
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
@@ -391,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         }
         float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(x[blk][j] - ((j & 1) ? ref1 : ref0));
+        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(x[blk][j], c, shift[j & 1]));
         st.l[0] += p[0] + p[2];
         st.l[1] += p[1] + p[3];
         // this lane's V words: rows of the product's k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -409,29 +431,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
           const uint32_t b1 = movmatrix_trans(cvt_bf16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
           st.mn[g][0] = fmaf(p[0], hi_f(k0), fmaf(p[2], hi_f(k1), st.mn[g][0]));
           st.mn[g][1] = fmaf(p[1], hi_f(k0), fmaf(p[3], hi_f(k1), st.mn[g][1]));
-          const uint32_t m128 = 0xc300c300u;  // -128, -128
-          mma_bf16_16816(st.off[g], m128, m128, m128, m128, b0, b1);
           const uint32_t x0 = g ? v0.y : v0.x, x1 = g ? v1.y : v1.x;
           const uint32_t x2 = g ? v2.y : v2.x, x3 = g ? v3.y : v3.x;
-          const uint32_t e0 = __byte_perm(x0, x1, 0x5410), f0 = __byte_perm(x0, x1, 0x7632);
-          const uint32_t e1 = __byte_perm(x2, x3, 0x5410), f1 = __byte_perm(x2, x3, 0x7632);
-          mma_bf16_16816(st.o[4 * g + 0], code_pair<0>(e0), code_pair<0>(f0), code_pair<0>(e1),
-                         code_pair<0>(f1), b0, b1);
-          mma_bf16_16816(st.o[4 * g + 1], code_pair<1>(e0), code_pair<1>(f0), code_pair<1>(e1),
-                         code_pair<1>(f1), b0, b1);
-          mma_bf16_16816(st.o[4 * g + 2], code_pair<2>(e0), code_pair<2>(f0), code_pair<2>(e1),
-                         code_pair<2>(f1), b0, b1);
-          mma_bf16_16816(st.o[4 * g + 3], code_pair<3>(e0), code_pair<3>(f0), code_pair<3>(e1),
-                         code_pair<3>(f1), b0, b1);
+          uint32_t e0 = __byte_perm(x0, x1, 0x5410), f0 = __byte_perm(x0, x1, 0x7632);
+          uint32_t e1 = __byte_perm(x2, x3, 0x5410), f1 = __byte_perm(x2, x3, 0x7632);
+          mma_bf16_16816(st.o[4 * g + 0], pair_lo(e0), pair_lo(f0), pair_lo(e1), pair_lo(f1), b0,
+                         b1);
+          mma_bf16_16816(st.o[4 * g + 1], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
+                         b1);
+          e0 >>= 8, f0 >>= 8, e1 >>= 8, f1 >>= 8;
+          mma_bf16_16816(st.o[4 * g + 2], pair_lo(e0), pair_lo(f0), pair_lo(e1), pair_lo(f1), b0,
+                         b1);
+          mma_bf16_16816(st.o[4 * g + 3], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
+                         b1);
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (i + kStages < my_tiles) issue(i + kStages);
+      if (issued < my_tiles) issue();
     }
 
     // ------------------------------------------------ combine the warps, write the piece
     // every copy of this warp has landed and been read (or given up on): its stages hold its
-    // result now, [8 heads][128], then m[8], l[8]
+    // result now, [8 heads][128], then m[8], l[8]; all but m times 2^64
     float* res = reinterpret_cast<float*>(mine);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -444,14 +465,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       float* dst = res + (2 * t4 + e) * kHeadDim + 8 * g8;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float add = st.off[g][e] + st.mn[g][e];
-        float4 y0, y1;
-        y0.x = st.o[4 * g + 0][e] + add, y0.y = st.o[4 * g + 0][2 + e] + add;
-        y0.z = st.o[4 * g + 1][e] + add, y0.w = st.o[4 * g + 1][2 + e] + add;
-        y1.x = st.o[4 * g + 2][e] + add, y1.y = st.o[4 * g + 2][2 + e] + add;
-        y1.z = st.o[4 * g + 3][e] + add, y1.w = st.o[4 * g + 3][2 + e] + add;
-        reinterpret_cast<float4*>(dst + 64 * g)[0] = y0;
-        reinterpret_cast<float4*>(dst + 64 * g)[1] = y1;
+        float y[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const float o = st.o[4 * g + (d >> 1)][2 * (d & 1) + e] * ((d & 2) ? 1.f / 16.f : 1.f);
+          y[d] = fmaf(o * kLift, kUncode, st.mn[g][e]);  // times 2^133
+        }
+        reinterpret_cast<float4*>(dst + 64 * g)[0] = make_float4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<float4*>(dst + 64 * g)[1] = make_float4(y[4], y[5], y[6], y[7]);
       }
       if (g8 == 0) {
         res[kMaxGroup * kHeadDim + 2 * t4 + e] = st.m[e];
@@ -483,15 +504,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
           acc.w = fmaf(f, y.w, acc.w);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float lse2 = L == 0.f ? -INFINITY : M + log2f(L);
+        const float lse2 = L == 0.f ? -INFINITY : M + log2f(L * (1.f / kLift));
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
         if (a.ws_o) {
           // unique per (unit, block): both only grow along the rows
-          const int64_t slot = ((int64_t)sq.b * a.hkv + sq.h + blockIdx.x) * kMaxGroup + head;
+          const int64_t slot = ((int64_t)u.b * a.hkv + u.h + blockIdx.x) * kMaxGroup + head;
           reinterpret_cast<float4*>(a.ws_o + slot * kHeadDim)[lane] = acc;
           if (lane == 0) a.ws_lse[slot] = lse2;
         } else {
-          const int64_t row = (int64_t)sq.b * a.hq + sq.h * a.group + head;
+          const int64_t row = (int64_t)u.b * a.hq + u.h * a.group + head;
           reinterpret_cast<uint2*>(a.out + row * kHeadDim)[lane] =
               make_uint2(cvt_bf16x2(acc.x, acc.y), cvt_bf16x2(acc.z, acc.w));
           if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
@@ -504,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     off = 0;
-    if (++sq.h == a.hkv) {
-      sq.h = 0;
+    if (++u.h == a.hkv) {
+      u.h = 0;
       do {
-        sq.p = a.pos[++sq.b];
-        sq.n = visible_rows(a, sq.p);
-      } while (sq.n == 0);
+        u.p = a.pos[++u.b];
+        u.n = static_cast<uint32_t>(visible_rows(a, u.p));
+      } while (u.n == 0);
     }
   }
 }
