@@ -119,58 +119,85 @@ __device__ __forceinline__ void enter(const DecodeQ4Args& a, Unit& u) {
                         : 0;
 }
 
-// What one of the three copying lanes (0: K, 1: V, 2: records) needs for a unit.
+// What one of the three copying lanes (0: K, 1: V, 2: records) keeps for a unit.
 struct Source {
-  const uint8_t* base[2];  // its unit's rows in the prefix and in the ring (or the pool)
+  const uint8_t* base0;    // its unit's rows in the prefix (or the pool), and in the ring
+  const uint8_t* base1;
   uint32_t row_bytes;
+  const uint8_t* next;     // where the next tile's first row is, and the rows from there to the
+  int32_t run;             // end of its run (less than a tile: to be looked up)
 };
 
 __device__ __forceinline__ Source source_of(const DecodeQ4Args& a, const Unit& u, int lane) {
   const StoreArgs& st = a.store;
   Source s;
   s.row_bytes = lane == 2 ? kQ4RecordBytes : kQ4RowBytes;
-  const int64_t unit = (int64_t)u.b * a.hkv + u.h;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint8_t* b = lane == 0 ? st.k[i] : lane == 1 ? st.v[i] : st.s[i];
-    s.base[i] = st.table ? b : b + unit * (i ? st.w : st.lp) * s.row_bytes;
+  s.base0 = lane == 0 ? st.k[0] : lane == 1 ? st.v[0] : st.s[0];
+  s.base1 = lane == 0 ? st.k[1] : lane == 1 ? st.v[1] : st.s[1];
+  if (!st.table) {
+    const int64_t unit = (int64_t)u.b * a.hkv + u.h;
+    s.base0 += unit * st.lp * s.row_bytes;
+    s.base1 += unit * st.w * s.row_bytes;
   }
+  s.next = nullptr;
+  s.run = 0;
   return s;
+}
+
+// The run of rows that visible row x starts: `next`, `run` (at least 1).  False where a block
+// table entry is bad.
+__device__ __forceinline__ bool locate(const DecodeQ4Args& a, const Unit& u, uint32_t x,
+                                       Source& src) {
+  const StoreArgs& st = a.store;
+  // prefix position x, or the window's (x - pre)-th oldest row
+  const bool ring = x >= u.pre;
+  uint32_t row = ring ? u.slot0 + (x - u.pre) : x;
+  if (ring && row >= static_cast<uint32_t>(st.w)) row -= st.w;
+  uint32_t run = ring ? min(st.w - row, u.n - x) : u.pre - x;
+  src.next = (ring ? src.base1 : src.base0) + (int64_t)row * src.row_bytes;
+  bool ok = true;
+  if (st.table) {
+    run = min(run, 64 - (row & 63));
+    const int32_t blk =
+        st.table[(int64_t)u.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
+    ok = blk >= 0 && blk < st.n_blocks;
+    src.next = src.base0 + (((int64_t)blk * a.hkv + u.h) * 64 + (row & 63)) * src.row_bytes;
+  }
+  src.run = static_cast<int32_t>(run);
+  return ok;
 }
 
 // Lanes 0..2 copy visible rows [x, x + cnt) of the unit into a stage; `mask` gets the rows that
 // are there (a bad block table entry leaves its rows out).
-__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, const Source& src,
+__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, Source& src,
                                           int lane, uint32_t x, uint32_t cnt, uint8_t* stage,
                                           uint64_t* bar, uint32_t* mask) {
-  const StoreArgs& st = a.store;
-  uint8_t* dst = stage + (lane == 2 ? 2 : lane) * kTile * kQ4RowBytes;
-  uint32_t copied = cnt, there = cnt == 32 ? 0xffffffffu : (1u << cnt) - 1u;
-  for (uint32_t done = 0; done < cnt;) {
-    // prefix position x, or the window's (x - pre)-th oldest row
-    const bool ring = x >= u.pre;
-    uint32_t row = ring ? u.slot0 + (x - u.pre) : x;
-    if (ring && row >= static_cast<uint32_t>(st.w)) row -= st.w;
-    uint32_t run = min(cnt - done, (ring ? st.w - row : u.pre - x));
-    const uint8_t* from = src.base[ring ? 1 : 0] + (int64_t)row * src.row_bytes;
-    bool ok = true;
-    if (st.table) {
-      run = min(run, 64 - (row & 63));
-      const int32_t blk =
-          st.table[(int64_t)u.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
-      ok = blk >= 0 && blk < st.n_blocks;
-      from = src.base[0] + (((int64_t)blk * a.hkv + u.h) * 64 + (row & 63)) * src.row_bytes;
+  uint8_t* dst = stage + lane * kTile * kQ4RowBytes;
+  uint32_t copied = cnt, there = 0xffffffffu;
+  bool ok = true;
+  if (src.run < kTile) ok = locate(a, u, x, src);
+  if (ok && src.run >= kTile && cnt == kTile) {
+    bulk_load(dst, src.next, kTile * src.row_bytes, bar);
+  } else {
+    there = cnt == 32 ? 0xffffffffu : (1u << cnt) - 1u;
+    for (uint32_t done = 0;;) {
+      const uint32_t run = min(cnt - done, static_cast<uint32_t>(src.run));
+      if (ok) {
+        bulk_load(dst + done * src.row_bytes, src.next, run * src.row_bytes, bar);
+      } else {
+        if (a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
+        there &= ~((run == 32 ? 0xffffffffu : (1u << run) - 1u) << done);
+        copied -= run;
+      }
+      done += run;
+      if (done >= cnt) break;
+      ok = locate(a, u, x + done, src);
     }
-    if (ok) {
-      bulk_load(dst + done * src.row_bytes, from, run * src.row_bytes, bar);
-    } else {
-      if (a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
-      there &= ~((run == 32 ? 0xffffffffu : (1u << run) - 1u) << done);
-      copied -= run;
-    }
-    done += run;
-    x += run;
+    src.run = 0;  // look the next tile up
   }
+  // the warp's next tile
+  src.next += kWarps * kTile * src.row_bytes;
+  src.run -= kWarps * kTile;
   if (lane == 0) {
     *mask = there;
     // the phase cannot end before this arrival, whichever copies have landed by then
@@ -178,10 +205,30 @@ __device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, 
   }
 }
 
+// The warp products and the 8 x 8 transpose as pure functions (not volatile), so that the
+// compiler may interleave independent chains.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Code pairs of a word as bf16 subnormals: codes 0 and 4 of its eight (low and high half), then
 // 1 and 5 (times 16); 2 and 6, 3 and 7 are the same of the word shifted down by 8.
 __device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return w & 0x000f000fu; }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
+
+// Both codes of the low bytes of the halves (u + 16 u', still a subnormal's or the first normals'
+// spacing), and of the high bytes.
+__device__ __forceinline__ uint32_t pair_byte(uint32_t w) { return w & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t pair_byte1(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -255,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
   uint32_t phase = 0;      // of stage `at`
   while (true) {
     enter(a, u);
-    const Source src = source_of(a, u, lane);
+    Source src = source_of(a, u, lane);
     const uint32_t piece = static_cast<uint32_t>(left < u.n - off ? left : u.n - off);
     const int tiles = static_cast<int>((piece + kTile - 1) / kTile);
     const int my_tiles = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
@@ -346,9 +393,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
             const uint32_t a0 = j ? (g ? w0.w : w0.z) : (g ? w0.y : w0.x);
             const uint32_t a1 = j ? (g ? w1.w : w1.z) : (g ? w1.y : w1.x);
             const uint32_t b0 = a0 >> 8, b1 = a1 >> 8;
-            mma_bf16_16816(acc[g], pair_lo(a0), pair_lo(a1), pair_hi(a0), pair_hi(a1),
+            mma(acc[g], pair_lo(a0), pair_lo(a1), pair_hi(a0), pair_hi(a1),
                            qf[g][j][0], qf[g][j][1]);
-            mma_bf16_16816(acc[g], pair_lo(b0), pair_lo(b1), pair_hi(b0), pair_hi(b1),
+            mma(acc[g], pair_lo(b0), pair_lo(b1), pair_hi(b0), pair_hi(b1),
                            qf[g][j][2], qf[g][j][3]);
           }
         }
@@ -427,22 +474,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         for (int g = 0; g < 2; ++g) {
           const uint32_t k0 = g ? c0.y : c0.x, k1 = g ? c1.y : c1.x;
           // a weight times its row's scale, rounded to bf16: the tensor cores' operand type
-          const uint32_t b0 = movmatrix_trans(cvt_bf16x2(p[0] * lo_f(k0), p[1] * lo_f(k0)));
-          const uint32_t b1 = movmatrix_trans(cvt_bf16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
+          const uint32_t b0 = transpose8(cvt_bf16x2(p[0] * lo_f(k0), p[1] * lo_f(k0)));
+          const uint32_t b1 = transpose8(cvt_bf16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
           st.mn[g][0] = fmaf(p[0], hi_f(k0), fmaf(p[2], hi_f(k1), st.mn[g][0]));
           st.mn[g][1] = fmaf(p[1], hi_f(k0), fmaf(p[3], hi_f(k1), st.mn[g][1]));
           const uint32_t x0 = g ? v0.y : v0.x, x1 = g ? v1.y : v1.x;
           const uint32_t x2 = g ? v2.y : v2.x, x3 = g ? v3.y : v3.x;
-          uint32_t e0 = __byte_perm(x0, x1, 0x5410), f0 = __byte_perm(x0, x1, 0x7632);
-          uint32_t e1 = __byte_perm(x2, x3, 0x5410), f1 = __byte_perm(x2, x3, 0x7632);
-          mma_bf16_16816(st.o[4 * g + 0], pair_lo(e0), pair_lo(f0), pair_lo(e1), pair_lo(f1), b0,
+          const uint32_t e0 = __byte_perm(x0, x1, 0x5410), f0 = __byte_perm(x0, x1, 0x7632);
+          const uint32_t e1 = __byte_perm(x2, x3, 0x5410), f1 = __byte_perm(x2, x3, 0x7632);
+          // even tiles take a byte, u + 16 u', odd ones its 16 u': one mask less a byte, and
+          // the even sums are told apart at the end
+          mma(st.o[4 * g + 0], pair_byte(e0), pair_byte(f0), pair_byte(e1),
+                         pair_byte(f1), b0, b1);
+          mma(st.o[4 * g + 1], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
                          b1);
-          mma_bf16_16816(st.o[4 * g + 1], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
-                         b1);
-          e0 >>= 8, f0 >>= 8, e1 >>= 8, f1 >>= 8;
-          mma_bf16_16816(st.o[4 * g + 2], pair_lo(e0), pair_lo(f0), pair_lo(e1), pair_lo(f1), b0,
-                         b1);
-          mma_bf16_16816(st.o[4 * g + 3], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
+          const uint32_t e2 = pair_byte1(e0), f2 = pair_byte1(f0);
+          const uint32_t e3 = pair_byte1(e1), f3 = pair_byte1(f1);
+          mma(st.o[4 * g + 2], e2, f2, e3, f3, b0, b1);
+          mma(st.o[4 * g + 3], pair_hi(e2), pair_hi(f2), pair_hi(e3), pair_hi(f3), b0,
                          b1);
         }
       }
@@ -468,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         float y[8];
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-          const float o = st.o[4 * g + (d >> 1)][2 * (d & 1) + e] * ((d & 2) ? 1.f / 16.f : 1.f);
+          const int i = 4 * g + (d >> 1), j = 2 * (d & 1) + e;
+          const float o = (d & 2) ? st.o[i][j] * (1.f / 16.f) : st.o[i][j] - st.o[i | 1][j];
           y[d] = fmaf(o * kLift, kUncode, st.mn[g][e]);  // times 2^133
         }
         reinterpret_cast<float4*>(dst + 64 * g)[0] = make_float4(y[0], y[1], y[2], y[3]);
