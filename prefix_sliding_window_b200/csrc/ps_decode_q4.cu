@@ -9,19 +9,25 @@
 //  * a code u enters the matrix product as a bf16 subnormal: four bits at the bottom of a half
 //    word are u 2^-133 and the next four, masked in place, 16 u 2^-133 (exact: the exponent field
 //    stays 0 or 1, which share a spacing; the tensor cores take subnormals in full).  A word of
-//    eight codes costs one shift and four ands.  Queries and weights carry a factor 2^64 against
-//    the small codes, taken off with the 2^-133 and the 16s after the sums
+//    eight K codes costs one shift and four ands, of V codes four byte moves and six ands.
+//    Queries and weights carry a factor 2^64 against the small codes, taken off with the 2^-133
+//    and the 16s after the sums.  (As e4m3 bytes, u 2^-9, a word would cost three operations, but
+//    there is no such warp product in hardware: it is unpacked to halves, 186 us where this
+//    takes 139 at 256 sequences of 28 / 4 heads)
 //  * the dims of a row are stored so that one 16-byte load gives a lane the words of a whole
 //    K fragment row; which dim goes to which position of the product does not matter as long as
 //    the query's fragment agrees
 //  * scales multiply scores (K) and weights (V), never the 128 codes of a row
 // Eight query heads of a KV head share a row's bytes (the columns of the products).
 //
-// Work: a unit is (sequence, KV head).  With fewer units than block slots, one wave of blocks takes
-// equal shares of all visible rows back to back (a share may span units; a unit's pieces are
-// combined by merge_q4_kernel); otherwise one block a unit.  Inside a block every warp streams its
-// own 32-row tiles (every eighth) through three stages of shared memory with bulk copies of exactly
-// the rows it needs: no warp waits for another until the piece ends.
+// Work: a unit is (sequence, KV head).  One wave of blocks takes equal shares of all units' visible
+// rows back to back; a share may span units, and a unit's pieces are combined by merge_q4_kernel
+// (above kMaxBatch sequences, whose lengths would take long to scan: one block a unit).  Inside a
+// block every warp streams its own 32-row tiles (every eighth of a piece) through three stages of
+// shared memory, on into the next piece: warps meet only where a piece ends.  The copies are
+// 16-byte asynchronous loads, nine a lane and tile.  (One lane's bulk copies cost a hundred
+// instructions a tile in setting up their uniform operands, a fifth of all; tiles of 256 rows for
+// the whole block amortised that, but had to land whole before any warp could start.)
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -38,16 +44,19 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlocksPerSm = 2;
 constexpr int kTile = 32;  // rows of a warp's tile
 constexpr int kStages = 3;
-constexpr int kStageBytes = kTile * (2 * kQ4RowBytes + kQ4RecordBytes);
+constexpr int kRowBytes = 2 * kQ4RowBytes + kQ4RecordBytes;
+constexpr int kStageBytes = kTile * kRowBytes;
 constexpr int kWarpBytes = kStages * kStageBytes;
 constexpr int kSmemBytes = kWarps * kWarpBytes;
-static_assert(kWarpBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fits its stages");
+static_assert(kStageBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fits a stage");
 constexpr int kMinRowsPerBlock = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxBatch = 1024;
+// queries and weights carry 2^64 against the subnormal codes
 constexpr float kLiftLog2 = 64.f;
-constexpr float kLift = 18446744073709551616.f;          // 2^64: queries and weights
-constexpr float kUncode = 590295810358705651712.f;       // 2^69 = 2^133 / 2^64
+constexpr float kLift = 18446744073709551616.f;     // 2^64
+constexpr float kUncode = 590295810358705651712.f;  // 2^69 = 2^133 / 2^64
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
 constexpr float kMaxSlack = 8.f;
@@ -57,8 +66,9 @@ struct DecodeQ4Args {
   const int64_t* pos;
   __nv_bfloat16* out;
   float* lse;
-  float* ws_o;    // [units + grid, 8, D] normalised pieces, or NULL: one block a unit
-  float* ws_lse;  // [units + grid, 8] base-2 lse of each piece
+  float* ws_o;    // [grid, 2, 8, D] a block's first and last piece where they are not whole units,
+                  // normalised; NULL: one block a unit
+  float* ws_lse;  // [grid, 2, 8] base-2 lse of each
   int32_t* status;
   int32_t batch, hq, hkv, group;
   float scale_log2;
@@ -104,12 +114,13 @@ __device__ __forceinline__ RowScan scan_rows(const DecodeQ4Args& a, int lane, bo
   return s;
 }
 
-// The unit a block works on.
+// A unit, and the rows [off, off + rows) of it that a block works on.
 struct Unit {
   int64_t p;       // position
   uint32_t n, pre; // visible rows, visible prefix rows
   uint32_t slot0;  // ring slot of the oldest window row
   int32_t b, h;
+  uint32_t off, rows;
 };
 
 __device__ __forceinline__ void enter(const DecodeQ4Args& a, Unit& u) {
@@ -119,90 +130,101 @@ __device__ __forceinline__ void enter(const DecodeQ4Args& a, Unit& u) {
                         : 0;
 }
 
-// What one of the three copying lanes (0: K, 1: V, 2: records) keeps for a unit.
-struct Source {
-  const uint8_t* base0;    // its unit's rows in the prefix (or the pool), and in the ring
-  const uint8_t* base1;
-  uint32_t row_bytes;
-  const uint8_t* next;     // where the next tile's first row is, and the rows from there to the
-  int32_t run;             // end of its run (less than a tile: to be looked up)
+// Where a warp is in a piece: the row of its array that the next tile starts at, and how many rows
+// from there on are contiguous (less than a tile: to be looked up).
+struct Cursor {
+  int64_t at;
+  int32_t run;
+  bool ring;  // in the ring's array (never for a paged store: one pool)
 };
 
-__device__ __forceinline__ Source source_of(const DecodeQ4Args& a, const Unit& u, int lane) {
-  const StoreArgs& st = a.store;
-  Source s;
-  s.row_bytes = lane == 2 ? kQ4RecordBytes : kQ4RowBytes;
-  s.base0 = lane == 0 ? st.k[0] : lane == 1 ? st.v[0] : st.s[0];
-  s.base1 = lane == 0 ? st.k[1] : lane == 1 ? st.v[1] : st.s[1];
-  if (!st.table) {
-    const int64_t unit = (int64_t)u.b * a.hkv + u.h;
-    s.base0 += unit * st.lp * s.row_bytes;
-    s.base1 += unit * st.w * s.row_bytes;
-  }
-  s.next = nullptr;
-  s.run = 0;
-  return s;
-}
-
-// The run of rows that visible row x starts: `next`, `run` (at least 1).  False where a block
-// table entry is bad.
+// Looks visible row x up; false where a block table entry is bad.
 __device__ __forceinline__ bool locate(const DecodeQ4Args& a, const Unit& u, uint32_t x,
-                                       Source& src) {
+                                       Cursor& c) {
   const StoreArgs& st = a.store;
   // prefix position x, or the window's (x - pre)-th oldest row
   const bool ring = x >= u.pre;
   uint32_t row = ring ? u.slot0 + (x - u.pre) : x;
   if (ring && row >= static_cast<uint32_t>(st.w)) row -= st.w;
   uint32_t run = ring ? min(st.w - row, u.n - x) : u.pre - x;
-  src.next = (ring ? src.base1 : src.base0) + (int64_t)row * src.row_bytes;
-  bool ok = true;
   if (st.table) {
     run = min(run, 64 - (row & 63));
     const int32_t blk =
         st.table[(int64_t)u.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
-    ok = blk >= 0 && blk < st.n_blocks;
-    src.next = src.base0 + (((int64_t)blk * a.hkv + u.h) * 64 + (row & 63)) * src.row_bytes;
+    c.at = ((int64_t)blk * a.hkv + u.h) * 64 + (row & 63);
+    c.run = static_cast<int32_t>(run);
+    c.ring = false;
+    return blk >= 0 && blk < st.n_blocks;
   }
-  src.run = static_cast<int32_t>(run);
-  return ok;
+  c.at = ((int64_t)u.b * a.hkv + u.h) * (ring ? st.w : st.lp) + row;
+  c.run = static_cast<int32_t>(run);
+  c.ring = ring;
+  return true;
 }
 
-// Lanes 0..2 copy visible rows [x, x + cnt) of the unit into a stage; `mask` gets the rows that
-// are there (a bad block table entry leaves its rows out).
-__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, Source& src,
-                                          int lane, uint32_t x, uint32_t cnt, uint8_t* stage,
-                                          uint64_t* bar, uint32_t* mask) {
-  uint8_t* dst = stage + lane * kTile * kQ4RowBytes;
-  uint32_t copied = cnt, there = 0xffffffffu;
+// 16 bytes to shared memory, asynchronously; zeros where !there (src is not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_if(uint32_t dst, const uint8_t* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Copies the tile from row row0 of a piece into a stage (all lanes).  Rows past the piece's end
+// and rows that a bad block table entry leaves out become zeros; `absent` gets the latter.
+__device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, uint32_t row0,
+                                          int lane, Cursor& c, uint32_t stage, uint32_t* absent) {
+  const StoreArgs& st = a.store;
+  const uint32_t cnt = u.rows - row0;  // a tile or more, or the last rows
+  const uint32_t dst = stage + lane * 16;
   bool ok = true;
-  if (src.run < kTile) ok = locate(a, u, x, src);
-  if (ok && src.run >= kTile && cnt == kTile) {
-    bulk_load(dst, src.next, kTile * src.row_bytes, bar);
-  } else {
-    there = cnt == 32 ? 0xffffffffu : (1u << cnt) - 1u;
-    for (uint32_t done = 0;;) {
-      const uint32_t run = min(cnt - done, static_cast<uint32_t>(src.run));
-      if (ok) {
-        bulk_load(dst + done * src.row_bytes, src.next, run * src.row_bytes, bar);
-      } else {
-        if (a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
-        there &= ~((run == 32 ? 0xffffffffu : (1u << run) - 1u) << done);
-        copied -= run;
-      }
-      done += run;
-      if (done >= cnt) break;
-      ok = locate(a, u, x + done, src);
+  if (c.run < kTile) ok = locate(a, u, u.off + row0, c);
+  if (ok && c.run >= kTile && cnt >= kTile) {
+    const int64_t at = c.at * kQ4RowBytes + lane * 16;
+    const uint8_t* k = (c.ring ? st.k[1] : st.k[0]) + at;
+    const uint8_t* v = (c.ring ? st.v[1] : st.v[0]) + at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      copy16(dst + 512 * j, k + 512 * j);
+      copy16(dst + kTile * kQ4RowBytes + 512 * j, v + 512 * j);
     }
-    src.run = 0;  // look the next tile up
+    copy16(dst + 2 * kTile * kQ4RowBytes,
+           (c.ring ? st.s[1] : st.s[0]) + c.at * kQ4RecordBytes + lane * 16);
+    if (st.table && lane == 0) *absent = 0;
+  } else {
+    // row by row: lane l copies a quarter of rows 8 j + l / 4, and row l's record
+#pragma unroll 1
+    for (int j = 0; j < 5; ++j) {
+      const uint32_t r = j < 4 ? 8 * j + (lane >> 2) : lane;
+      Cursor x{0, 0, false};
+      const bool in = r < cnt;
+      bool there = in;
+      if (in) there = locate(a, u, u.off + row0 + r, x);
+      if (!there) x.at = 0, x.ring = !st.k[0];
+      if (j < 4) {
+        const int64_t at = x.at * kQ4RowBytes + (lane & 3) * 16;
+        copy16_if(dst + 512 * j, (x.ring ? st.k[1] : st.k[0]) + at, there);
+        copy16_if(dst + kTile * kQ4RowBytes + 512 * j, (x.ring ? st.v[1] : st.v[0]) + at, there);
+      } else {
+        copy16_if(dst + 2 * kTile * kQ4RowBytes,
+                  (x.ring ? st.s[1] : st.s[0]) + x.at * kQ4RecordBytes, there);
+        const uint32_t gone = __ballot_sync(0xffffffffu, in && !there);
+        if (gone && lane == 0 && a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
+        if (st.table && lane == 0) *absent = gone;
+      }
+    }
+    c.run = 0;
   }
-  // the warp's next tile
-  src.next += kWarps * kTile * src.row_bytes;
-  src.run -= kWarps * kTile;
-  if (lane == 0) {
-    *mask = there;
-    // the phase cannot end before this arrival, whichever copies have landed by then
-    mbar_arrive_expect_tx(bar, copied * (2 * kQ4RowBytes + kQ4RecordBytes));
-  }
+  c.at += kWarps * kTile;  // the warp's next tile
+  c.run -= kWarps * kTile;
 }
 
 // The warp products and the 8 x 8 transpose as pure functions (not volatile), so that the
@@ -220,14 +242,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Code pairs of a word as bf16 subnormals: codes 0 and 4 of its eight (low and high half), then
-// 1 and 5 (times 16); 2 and 6, 3 and 7 are the same of the word shifted down by 8.
+// Codes as bf16 pairs, one from each half word, of a byte's two: the lower one, the upper one
+// (16 u), or both together (u + 16 u', still on the subnormals' spacing); the high byte moved down.
 __device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
-
-// Both codes of the low bytes of the halves (u + 16 u', still a subnormal's or the first normals'
-// spacing), and of the high bytes.
 __device__ __forceinline__ uint32_t pair_byte(uint32_t w) { return w & 0x00ff00ffu; }
+__device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
 __device__ __forceinline__ uint32_t pair_byte1(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
@@ -235,7 +254,7 @@ __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0
 
 // One warp's running softmax and accumulators over the heads (2 t, 2 t + 1) of its lane's t.
 struct State {
-  float m[2], l[2];
+  float l[2];
   float o[8][4];   // tile 4 g + i: dims 64 g + 8 (lane / 4) + 2 i + {0, 1}, heads 2 t + {0, 1}
   float mn[2][2];  // sum p m of a group, over this lane's rows
 };
@@ -246,23 +265,20 @@ __device__ __forceinline__ int tile_row(int r) { return (r & 1) ? 4 + ((r >> 1) 
 
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const DecodeQ4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_full[kWarps][kStages];
-  __shared__ uint32_t s_mask[kWarps][kStages];
+  __shared__ uint32_t s_absent[kWarps][kStages];
+  __shared__ float* s_result[kWarps];
+  // this piece and the next, a copy a warp: only the lane that issues copies reads most of it
+  __shared__ Unit s_piece[kWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   uint8_t* mine = smem + warp * kWarpBytes;
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&s_full[warp][s], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
   pdl_wait();
   pdl_trigger();
 
   // ------------------------------------------------ this block's share of the rows
   Unit u;
-  uint32_t off = 0;  // first row in the current unit
-  int64_t left;      // rows of the share still to do
+  int64_t left;  // rows of the share still to do
+  u.off = 0;
   if (a.ws_o) {
     const RowScan sc = scan_rows(a, lane, blockIdx.x == 0 && warp == 0);
     const int64_t total = sc.total * a.hkv;
@@ -285,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
     }
     u.n = static_cast<uint32_t>(n);
     u.h = static_cast<int32_t>(div_nonneg(rest, n));
-    off = static_cast<uint32_t>(rest - u.h * n);
+    u.off = static_cast<uint32_t>(rest - u.h * n);
   } else {
     u.b = blockIdx.x / a.hkv;
     u.h = blockIdx.x % a.hkv;
@@ -298,90 +314,119 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
 
   // scores come out of the products times 2^(64 - 133); c takes that off and scales to base 2
   const float c = a.scale_log2 * kUncode;
-  int in = 0, at = 0;      // stage the next tile goes to, stage the next tile comes from
-  uint32_t phase = 0;      // of stage `at`
-  while (true) {
-    enter(a, u);
-    Source src = source_of(a, u, lane);
-    const uint32_t piece = static_cast<uint32_t>(left < u.n - off ? left : u.n - off);
-    const int tiles = static_cast<int>((piece + kTile - 1) / kTile);
-    const int my_tiles = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    int issued = 0;
-    auto issue = [&]() {  // this warp's next tile of the piece
-      if (lane < 3) {
-        const uint32_t r = static_cast<uint32_t>(warp + kWarps * issued) * kTile;
-        load_tile(a, u, src, lane, off + r, min(piece - r, static_cast<uint32_t>(kTile)),
-                  mine + in * kStageBytes, &s_full[warp][in], &s_mask[warp][in]);
+  int in = 0, at = 0;  // stage the next tile goes to, stage the next tile comes from
+  int flying = 0;       // tiles issued and not yet used
+  uint32_t row = warp * kTile;  // the next tile to issue: its row, and whether in the next piece
+  bool next = false;
+  Cursor cursor{0, 0, false};
+  int cur = 0;        // which of s_piece is this one
+  enter(a, u);
+  u.rows = static_cast<uint32_t>(left < u.n - u.off ? left : u.n - u.off);
+  if (lane == 0) s_piece[warp][0] = u;
+  __syncwarp();
+  for (bool first_piece = true;; first_piece = false) {
+    const uint32_t piece = s_piece[warp][cur].rows;
+    left -= piece;
+    if (lane == 0) {  // the next piece: the next unit that has rows, from its first row
+      Unit v = s_piece[warp][cur];
+      v.off = v.rows = 0;
+      if (left > 0) {
+        if (++v.h == a.hkv) {
+          v.h = 0;
+          do {
+            v.p = a.pos[++v.b];
+            v.n = static_cast<uint32_t>(visible_rows(a, v.p));
+          } while (v.n == 0);
+          enter(a, v);
+        }
+        v.rows = static_cast<uint32_t>(left < v.n ? left : v.n);
       }
-      in = in == kStages - 1 ? 0 : in + 1;
-      ++issued;
+      s_piece[warp][cur ^ 1] = v;
+    }
+    __syncwarp();
+    // Issues the warp's next tile, of this piece or the next.  One stage stays free while a tile of
+    // the next piece would take it: the warp's result goes there.
+    // Every call commits a group of copies, empty or not: when a tile is used, two groups at least
+    // have been committed after its own.
+    auto issue = [&]() {
+      if (!next && row >= piece) {
+        next = true;
+        row = warp * kTile;
+        cursor.run = 0;
+      }
+      const Unit& from = s_piece[warp][next ? cur ^ 1 : cur];
+      if (flying < (next ? kStages - 1 : kStages) && row < from.rows) {
+        load_tile(a, from, row, lane, cursor, smem_u32(mine) + in * kStageBytes,
+                  &s_absent[warp][in]);
+        in = in == kStages - 1 ? 0 : in + 1;
+        row += kWarps * kTile;
+        ++flying;
+      }
+      copies_commit();
     };
-    while (issued < my_tiles && issued < kStages) issue();
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) issue();
 
     // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^64 (2^60
     // where the codes come out 16 times as large); and each group's sum of query dims
     uint32_t qf[2][2][4];
-    float qs[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      qs[g] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (g8 < a.group)
-          w = *reinterpret_cast<const uint4*>(
-              a.q + ((int64_t)u.b * a.hq + u.h * a.group + g8) * kHeadDim + 64 * g + 16 * t4 +
-              8 * j);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = (i & 1) ? kLift / 16.f : kLift;
-          qs[g] += lo_f(ww[i]) + hi_f(ww[i]);
-          qf[g][j][i] = cvt_bf16x2(lo_f(ww[i]) * f, hi_f(ww[i]) * f);
-        }
-      }
-      qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
-      qs[g] = (qs[g] + __shfl_xor_sync(0xffffffffu, qs[g], 2)) * (1.f / kUncode);
-    }
     float Q[2][2];  // of heads 2 t + e, on the products' scale
+    {
+      const int head0 = s_piece[warp][cur].b * a.hq + s_piece[warp][cur].h * a.group;
+      float qs[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < 2; ++g) {
+        qs[g] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) Q[g][e] = __shfl_sync(0xffffffffu, qs[g], 4 * (2 * t4 + e));
+        for (int j = 0; j < 2; ++j) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (g8 < a.group)
+            w = *reinterpret_cast<const uint4*>(a.q + (int64_t)(head0 + g8) * kHeadDim + 64 * g +
+                                                16 * t4 + 8 * j);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = (i & 1) ? kLift / 16.f : kLift;
+            qs[g] += lo_f(ww[i]) + hi_f(ww[i]);
+            qf[g][j][i] = cvt_bf16x2(lo_f(ww[i]) * f, hi_f(ww[i]) * f);
+          }
+        }
+        qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
+        qs[g] = (qs[g] + __shfl_xor_sync(0xffffffffu, qs[g], 2)) * (1.f / kUncode);
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) Q[g][e] = __shfl_sync(0xffffffffu, qs[g], 4 * (2 * t4 + e));
+    }
 
     State st;
-    st.m[0] = st.m[1] = -INFINITY;
     st.l[0] = st.l[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
     st.mn[0][0] = st.mn[0][1] = st.mn[1][0] = st.mn[1][1] = 0.f;
-    // a score (before c) above this moves the running maximum
+    // a score (before c) above this moves the running maximum m
     float above[2] = {-INFINITY, -INFINITY};
-    // weights are 2^(c x - m + 64): taken with -m + 64 in one step
-    float shift[2] = {kLiftLog2, kLiftLog2};
+    // weights are 2^(c x + shift), shift = 64 - m (while there is no m, no score counts)
+    float shift[2] = {INFINITY, INFINITY};
 
     const int kr = tile_row(g8);  // this lane's K rows: kr, kr + 8
-    for (int i = 0; i < my_tiles; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[warp][at], phase, a.status))) {
-        // given up on (and flagged): see the other copies in flight to their end as well
-        for (int j = i + 1; j < issued; ++j) {
-          if (++at == kStages) at = 0, phase ^= 1;
-          mbar_wait(&s_full[warp][at], phase, a.status);
-        }
-        if (++at == kStages) at = 0, phase ^= 1;
-        break;
-      }
-      const uint8_t* stage = mine + at * kStageBytes;
-      const uint8_t* rec = stage + 2 * kTile * kQ4RowBytes;
-      const uint32_t mask = s_mask[warp][at];
-      if (++at == kStages) at = 0, phase ^= 1;
+    for (uint32_t first = warp * kTile; first < piece; first += kWarps * kTile) {
+      copies_wait<kStages - 1>();
+      __syncwarp();  // every lane's copies
+      const uint8_t* kst = mine + at * kStageBytes;
+      const uint8_t* vst = kst + kTile * kQ4RowBytes;
+      const uint8_t* rec = vst + kTile * kQ4RowBytes;
+      uint32_t mask = piece - first >= kTile ? 0xffffffffu : (1u << (piece - first)) - 1u;
+      if (a.store.table) mask &= ~s_absent[warp][at];
+      at = at == kStages - 1 ? 0 : at + 1;
       // ---------------------------------------- scores of 2 x 16 rows
       float x[2][4];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         const int r0 = 16 * blk + kr, r1 = r0 + 8;
-        const uint4 w0 = *reinterpret_cast<const uint4*>(stage + r0 * kQ4RowBytes + 16 * t4);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(stage + r1 * kQ4RowBytes + 16 * t4);
+        const uint4 w0 = *reinterpret_cast<const uint4*>(kst + r0 * kQ4RowBytes + 16 * t4);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(kst + r1 * kQ4RowBytes + 16 * t4);
         const uint2 c0 = *reinterpret_cast<const uint2*>(rec + r0 * kQ4RecordBytes);
         const uint2 c1 = *reinterpret_cast<const uint2*>(rec + r1 * kQ4RecordBytes);
         float acc[2][4];
@@ -393,10 +438,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
             const uint32_t a0 = j ? (g ? w0.w : w0.z) : (g ? w0.y : w0.x);
             const uint32_t a1 = j ? (g ? w1.w : w1.z) : (g ? w1.y : w1.x);
             const uint32_t b0 = a0 >> 8, b1 = a1 >> 8;
-            mma(acc[g], pair_lo(a0), pair_lo(a1), pair_hi(a0), pair_hi(a1),
-                           qf[g][j][0], qf[g][j][1]);
-            mma(acc[g], pair_lo(b0), pair_lo(b1), pair_hi(b0), pair_hi(b1),
-                           qf[g][j][2], qf[g][j][3]);
+            mma(acc[g], pair_lo(a0), pair_lo(a1), pair_hi(a0), pair_hi(a1), qf[g][j][0],
+                qf[g][j][1]);
+            mma(acc[g], pair_lo(b0), pair_lo(b1), pair_hi(b0), pair_hi(b1), qf[g][j][2],
+                qf[g][j][3]);
           }
         }
 #pragma unroll
@@ -429,13 +474,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-          const float m = fmaxf(st.m[e], mx[e] * c);
-          f[e] = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - m);
-          st.m[e] = m;
-          if (m != -INFINITY) {
-            shift[e] = kLiftLog2 - m;
-            above[e] = (m + kMaxSlack) / c;
-          }
+          const float to = fminf(shift[e], kLiftLog2 - mx[e] * c);
+          f[e] = shift[e] == INFINITY ? 0.f : fast_exp2(to - shift[e]);
+          if (to != INFINITY) above[e] = (kLiftLog2 + kMaxSlack - to) / c;
+          shift[e] = to;
           st.l[e] *= f[e];
           st.mn[0][e] *= f[e];
           st.mn[1][e] *= f[e];
@@ -448,23 +490,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
           st.o[j][3] *= f[1];
         }
       }
+      const float sh[2] = {shift[0] == INFINITY ? 0.f : shift[0],
+                           shift[1] == INFINITY ? 0.f : shift[1]};
       // ---------------------------------------- weights and values
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         const int r0 = 16 * blk + kr, r1 = r0 + 8;
-        uint2 c0 = *reinterpret_cast<const uint2*>(rec + r0 * kQ4RecordBytes + 8);
-        uint2 c1 = *reinterpret_cast<const uint2*>(rec + r1 * kQ4RecordBytes + 8);
-        if (mask != 0xffffffffu) {  // what an absent row's record holds may be a NaN
-          if (!((mask >> r0) & 1u)) c0 = make_uint2(0, 0);
-          if (!((mask >> r1) & 1u)) c1 = make_uint2(0, 0);
-        }
+        const uint2 c0 = *reinterpret_cast<const uint2*>(rec + r0 * kQ4RecordBytes + 8);
+        const uint2 c1 = *reinterpret_cast<const uint2*>(rec + r1 * kQ4RecordBytes + 8);
         float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(x[blk][j], c, shift[j & 1]));
+        for (int j = 0; j < 4; ++j) p[j] = fast_exp2(fmaf(x[blk][j], c, sh[j & 1]));
         st.l[0] += p[0] + p[2];
         st.l[1] += p[1] + p[3];
         // this lane's V words: rows of the product's k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        const uint8_t* vb = stage + (kTile + 16 * blk) * kQ4RowBytes + 8 * g8;
+        const uint8_t* vb = vst + 16 * blk * kQ4RowBytes + 8 * g8;
         const int va = t4, vc = 4 + (t4 ^ 1);
         const uint2 v0 = *reinterpret_cast<const uint2*>(vb + va * kQ4RowBytes);
         const uint2 v1 = *reinterpret_cast<const uint2*>(vb + vc * kQ4RowBytes);
@@ -496,13 +536,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (issued < my_tiles) issue();
+      --flying;
+      issue();
     }
 
     // ------------------------------------------------ combine the warps, write the piece
-    // every copy of this warp has landed and been read (or given up on): its stages hold its
-    // result now, [8 heads][128], then m[8], l[8]; all but m times 2^64
-    float* res = reinterpret_cast<float*>(mine);
+    // the stage to be filled next holds the warp's result now, [8 heads][128], then m[8], l[8], all
+    // but m times 2^64; the other stages may hold the next piece's first tiles
+    float* res = reinterpret_cast<float*>(mine + in * kStageBytes);
+    if (lane == 0) s_result[warp] = res;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -525,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         reinterpret_cast<float4*>(dst + 64 * g)[1] = make_float4(y[4], y[5], y[6], y[7]);
       }
       if (g8 == 0) {
-        res[kMaxGroup * kHeadDim + 2 * t4 + e] = st.m[e];
+        res[kMaxGroup * kHeadDim + 2 * t4 + e] = kLiftLog2 - shift[e];
         res[kMaxGroup * kHeadDim + kMaxGroup + 2 * t4 + e] = st.l[e];
       }
     }
@@ -536,13 +578,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         float ml[kWarps], M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          ml[w] = reinterpret_cast<float*>(smem + w * kWarpBytes)[kMaxGroup * kHeadDim + head];
+          ml[w] = s_result[w][kMaxGroup * kHeadDim + head];
           M = fmaxf(M, ml[w]);
         }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float* r = reinterpret_cast<float*>(smem + w * kWarpBytes);
+          const float* r = s_result[w];
           const float f = ml[w] == -INFINITY ? 0.f : fast_exp2(ml[w] - M);
           const float lw = r[kMaxGroup * kHeadDim + kMaxGroup + head];
           if (lw == 0.f) continue;  // no row of this warp counted
@@ -556,38 +598,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const float lse2 = L == 0.f ? -INFINITY : M + log2f(L * (1.f / kLift));
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-        if (a.ws_o) {
-          // unique per (unit, block): both only grow along the rows
-          const int64_t slot = ((int64_t)u.b * a.hkv + u.h + blockIdx.x) * kMaxGroup + head;
+        if (piece < s_piece[warp][cur].n) {
+          const int64_t slot = (2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1)) * kMaxGroup + head;
           reinterpret_cast<float4*>(a.ws_o + slot * kHeadDim)[lane] = acc;
           if (lane == 0) a.ws_lse[slot] = lse2;
         } else {
-          const int64_t row = (int64_t)u.b * a.hq + u.h * a.group + head;
+          const int64_t row = (int64_t)s_piece[warp][cur].b * a.hq +
+                              s_piece[warp][cur].h * a.group + head;
           reinterpret_cast<uint2*>(a.out + row * kHeadDim)[lane] =
               make_uint2(cvt_bf16x2(acc.x, acc.y), cvt_bf16x2(acc.z, acc.w));
           if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
         }
       }
     }
-    left -= piece;
     if (left <= 0) break;
-    // next unit that has rows; its copies overwrite the results just read
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
-    off = 0;
-    if (++u.h == a.hkv) {
-      u.h = 0;
-      do {
-        u.p = a.pos[++u.b];
-        u.n = static_cast<uint32_t>(visible_rows(a, u.p));
-      } while (u.n == 0);
-    }
+    __syncthreads();  // the next piece's tiles overwrite the results just read
+    cur ^= 1;
+    next = false;  // `row` is a row of the next piece already
   }
 }
 
-// Combines the pieces of one (sequence, query head), one warp each: block c of the decode owned
-// the rows [total c / grid, total (c + 1) / grid) and stored its piece of unit u at slot u + c, so
-// which pieces exist follows from the positions alone.  Lane i owns dims 4 i .. 4 i + 3.
+// Combines the pieces of one (sequence, query head), one warp each, where its unit was split:
+// block c of the decode owned the rows [total c / grid, total (c + 1) / grid), so which blocks hold
+// pieces follows from the positions alone.  A unit's later pieces are their blocks' first ones, its
+// earliest is its block's first or last.  Lane i owns dims 4 i .. 4 i + 3.
 __global__ void __launch_bounds__(128)
     merge_q4_kernel(const DecodeQ4Args a, int32_t grid) {
   const int lane = threadIdx.x & 31;
@@ -602,16 +636,16 @@ __global__ void __launch_bounds__(128)
   int64_t first = __shfl_sync(0xffffffffu, sc.before, src);
   for (int i = src * sc.per; i < b; ++i) first += visible_rows(a, a.pos[i]);
   const int64_t n = visible_rows(a, a.pos[b]);
-  const int64_t unit = (int64_t)b * a.hkv + h;
-  int c_lo = 1, c_hi = 0;
+  int c_lo = 1, c_hi = 0, late = 0;  // late: the piece in c_lo is that block's last
   if (n > 0) {
     const int64_t pu = a.hkv * first + h * n;
     c_lo = static_cast<int>(div_nonneg((pu + 1) * grid - 1, total));
     c_hi = static_cast<int>(div_nonneg((pu + n) * grid - 1, total));
+    late = div_nonneg(total * c_lo, grid) < pu;
   }
   pdl_trigger();
   pdl_wait();
-  if (!live) return;
+  if (!live || (n > 0 && c_lo == c_hi)) return;  // a whole unit is written already
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, L = 0.f;
   for (int c0 = c_lo; c0 <= c_hi; c0 += 4) {
@@ -624,7 +658,7 @@ __global__ void __launch_bounds__(128)
       ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       // with fewer rows than blocks some blocks own none and wrote no piece
       if (c <= c_hi && (total >= grid || total * c / grid != total * (c + 1) / grid)) {
-        const int64_t slot = (unit + c) * kMaxGroup + hh;
+        const int64_t slot = (2 * (int64_t)c + (c == c_lo ? late : 0)) * kMaxGroup + hh;
         lv[k] = a.ws_lse[slot];
         ov[k] = reinterpret_cast<const float4*>(a.ws_o + slot * kHeadDim)[lane];
       }
@@ -670,6 +704,7 @@ int blocks_per_sm() {
 
 // Blocks of the one-wave schedule, or 0 for one block a unit.
 int64_t share_grid(int64_t batch, int32_t hkv, int64_t max_keys) {
+  if (batch > kMaxBatch) return 0;
   const int64_t units = batch * hkv;
   const int64_t slots = (int64_t)sm_count() * blocks_per_sm();
   if (units >= slots) return 0;
@@ -679,7 +714,7 @@ int64_t share_grid(int64_t batch, int32_t hkv, int64_t max_keys) {
     // a multiple of the unit count that fills 5/6 of the slots: equally long units then split on
     // their own borders, and no block changes unit midway
     const int64_t even = units * (slots / units);
-    if (even * 6 >= slots * 5) g = even;
+    if (units <= slots && even * 6 >= slots * 5) g = even;
   }
   return g < 1 ? 1 : g;
 }
@@ -689,7 +724,7 @@ int64_t share_grid(int64_t batch, int32_t hkv, int64_t max_keys) {
 size_t decode_q4_workspace_bytes(int64_t batch, int32_t hkv, int64_t max_keys) {
   const int64_t g = share_grid(batch, hkv, max_keys);
   if (g == 0 || batch == 0) return 0;
-  const size_t slots = size_t(batch * hkv + g) * kMaxGroup;
+  const size_t slots = size_t(2 * g) * kMaxGroup;
   return slots * (kHeadDim + 1) * sizeof(float);
 }
 
@@ -704,7 +739,7 @@ int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream) {
   a.out = static_cast<__nv_bfloat16*>(l.out);
   a.lse = l.lse;
   a.ws_o = g ? static_cast<float*>(l.workspace) : nullptr;
-  a.ws_lse = g ? a.ws_o + size_t(units + g) * kMaxGroup * kHeadDim : nullptr;
+  a.ws_lse = g ? a.ws_o + size_t(2 * g) * kMaxGroup * kHeadDim : nullptr;
   a.status = l.status;
   a.batch = static_cast<int32_t>(l.batch);
   a.hq = l.hq;
