@@ -130,36 +130,34 @@ __device__ __forceinline__ void enter(const DecodeQ4Args& a, Unit& u) {
                         : 0;
 }
 
-// Where a warp is in a piece: the row of its array that the next tile starts at, and how many rows
-// from there on are contiguous (less than a tile: to be looked up).
-struct Cursor {
+// A run of rows that are contiguous in their array; ok: false where a block table entry is bad.
+struct Rows {
   int64_t at;
-  int32_t run;
-  bool ring;  // in the ring's array (never for a paged store: one pool)
+  uint32_t run;
+  bool ring, ok;  // ring: in the ring's array (never for a paged store: one pool)
 };
 
-// Looks visible row x up; false where a block table entry is bad.
-__device__ __forceinline__ bool locate(const DecodeQ4Args& a, const Unit& u, uint32_t x,
-                                       Cursor& c) {
+// The run that visible row x starts.
+__device__ __forceinline__ Rows locate(const DecodeQ4Args& a, const Unit& u, uint32_t x) {
   const StoreArgs& st = a.store;
   // prefix position x, or the window's (x - pre)-th oldest row
   const bool ring = x >= u.pre;
   uint32_t row = ring ? u.slot0 + (x - u.pre) : x;
   if (ring && row >= static_cast<uint32_t>(st.w)) row -= st.w;
-  uint32_t run = ring ? min(st.w - row, u.n - x) : u.pre - x;
+  Rows r;
+  r.run = ring ? min(st.w - row, u.n - x) : u.pre - x;
+  r.ring = ring && !st.table;
+  r.ok = true;
   if (st.table) {
-    run = min(run, 64 - (row & 63));
+    r.run = min(r.run, 64 - (row & 63));
     const int32_t blk =
         st.table[(int64_t)u.b * st.table_stride + (ring ? st.pre_blocks : 0) + (row >> 6)];
-    c.at = ((int64_t)blk * a.hkv + u.h) * 64 + (row & 63);
-    c.run = static_cast<int32_t>(run);
-    c.ring = false;
-    return blk >= 0 && blk < st.n_blocks;
+    r.ok = blk >= 0 && blk < st.n_blocks;
+    r.at = ((int64_t)blk * a.hkv + u.h) * 64 + (row & 63);
+  } else {
+    r.at = ((int64_t)u.b * a.hkv + u.h) * (ring ? st.w : st.lp) + row;
   }
-  c.at = ((int64_t)u.b * a.hkv + u.h) * (ring ? st.w : st.lp) + row;
-  c.run = static_cast<int32_t>(run);
-  c.ring = ring;
-  return true;
+  return r;
 }
 
 // 16 bytes to shared memory, asynchronously; zeros where !there (src is not read).
@@ -178,53 +176,65 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A lane's place in a piece: where its 16 bytes of the warp's next tile are, if that is one of
+// `more` tiles that follow in the same run of rows.
+struct Cursor {
+  const uint8_t *k, *v, *s;
+  int32_t more;
+};
+
+// Copies the tile at the cursor, 16 bytes a lane and load, and moves on to the warp's next.
+__device__ __forceinline__ void copy_tile(Cursor& c, uint32_t dst) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    copy16(dst + 512 * j, c.k + 512 * j);
+    copy16(dst + kTile * kQ4RowBytes + 512 * j, c.v + 512 * j);
+  }
+  copy16(dst + 2 * kTile * kQ4RowBytes, c.s);
+  c.k += kWarps * kTile * kQ4RowBytes;
+  c.v += kWarps * kTile * kQ4RowBytes;
+  c.s += kWarps * kTile * kQ4RecordBytes;
+}
+
 // Copies the tile from row row0 of a piece into a stage (all lanes).  Rows past the piece's end
 // and rows that a bad block table entry leaves out become zeros; `absent` gets the latter.
 __device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, uint32_t row0,
-                                          int lane, Cursor& c, uint32_t stage, uint32_t* absent) {
+                                          int lane, Cursor& c, uint32_t dst, uint32_t* absent) {
   const StoreArgs& st = a.store;
   const uint32_t cnt = u.rows - row0;  // a tile or more, or the last rows
-  const uint32_t dst = stage + lane * 16;
-  bool ok = true;
-  if (c.run < kTile) ok = locate(a, u, u.off + row0, c);
-  if (ok && c.run >= kTile && cnt >= kTile) {
-    const int64_t at = c.at * kQ4RowBytes + lane * 16;
-    const uint8_t* k = (c.ring ? st.k[1] : st.k[0]) + at;
-    const uint8_t* v = (c.ring ? st.v[1] : st.v[0]) + at;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      copy16(dst + 512 * j, k + 512 * j);
-      copy16(dst + kTile * kQ4RowBytes + 512 * j, v + 512 * j);
-    }
-    copy16(dst + 2 * kTile * kQ4RowBytes,
-           (c.ring ? st.s[1] : st.s[0]) + c.at * kQ4RecordBytes + lane * 16);
-    if (st.table && lane == 0) *absent = 0;
-  } else {
-    // row by row: lane l copies a quarter of rows 8 j + l / 4, and row l's record
+  const Rows f = locate(a, u, u.off + row0);
+  if (st.table && lane == 0) *absent = 0;
+  c.more = 0;
+  if (f.ok && min(f.run, cnt) >= kTile) {
+    const int64_t at = f.at * kQ4RowBytes + lane * 16;
+    c.k = (f.ring ? st.k[1] : st.k[0]) + at;
+    c.v = (f.ring ? st.v[1] : st.v[0]) + at;
+    c.s = (f.ring ? st.s[1] : st.s[0]) + f.at * kQ4RecordBytes + lane * 16;
+    c.more = static_cast<int32_t>((min(f.run, cnt) - kTile) / (kWarps * kTile));
+    copy_tile(c, dst);
+    return;
+  }
+  // row by row: lane l copies a quarter of rows 8 j + l / 4, and row l's record
 #pragma unroll 1
-    for (int j = 0; j < 5; ++j) {
-      const uint32_t r = j < 4 ? 8 * j + (lane >> 2) : lane;
-      Cursor x{0, 0, false};
-      const bool in = r < cnt;
-      bool there = in;
-      if (in) there = locate(a, u, u.off + row0 + r, x);
-      if (!there) x.at = 0, x.ring = !st.k[0];
-      if (j < 4) {
-        const int64_t at = x.at * kQ4RowBytes + (lane & 3) * 16;
-        copy16_if(dst + 512 * j, (x.ring ? st.k[1] : st.k[0]) + at, there);
-        copy16_if(dst + kTile * kQ4RowBytes + 512 * j, (x.ring ? st.v[1] : st.v[0]) + at, there);
-      } else {
-        copy16_if(dst + 2 * kTile * kQ4RowBytes,
-                  (x.ring ? st.s[1] : st.s[0]) + x.at * kQ4RecordBytes, there);
-        const uint32_t gone = __ballot_sync(0xffffffffu, in && !there);
-        if (gone && lane == 0 && a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
-        if (st.table && lane == 0) *absent = gone;
+  for (int j = 0; j < 5; ++j) {
+    const uint32_t r = j < 4 ? 8 * j + (lane >> 2) : lane;
+    Rows x{0, 0, !st.k[0], false};
+    if (r < cnt) x = locate(a, u, u.off + row0 + r);
+    if (!x.ok) x.at = 0;
+    if (j < 4) {
+      const int64_t at = x.at * kQ4RowBytes + (lane & 3) * 16;
+      copy16_if(dst + 512 * j, (x.ring ? st.k[1] : st.k[0]) + at, x.ok);
+      copy16_if(dst + kTile * kQ4RowBytes + 512 * j, (x.ring ? st.v[1] : st.v[0]) + at, x.ok);
+    } else {
+      copy16_if(dst + 2 * kTile * kQ4RowBytes,
+                (x.ring ? st.s[1] : st.s[0]) + x.at * kQ4RecordBytes, x.ok);
+      const uint32_t gone = __ballot_sync(0xffffffffu, r < cnt && !x.ok);
+      if (gone && lane == 0) {  // (only a paged store has any)
+        if (a.status) atomicOr(a.status, PS_DEV_POS_RANGE);
+        *absent = gone;
       }
     }
-    c.run = 0;
   }
-  c.at += kWarps * kTile;  // the warp's next tile
-  c.run -= kWarps * kTile;
 }
 
 // The warp products and the 8 x 8 transpose as pure functions (not volatile), so that the
@@ -271,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
   __shared__ Unit s_piece[kWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
-  uint8_t* mine = smem + warp * kWarpBytes;
   pdl_wait();
   pdl_trigger();
 
@@ -314,11 +323,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
 
   // scores come out of the products times 2^(64 - 133); c takes that off and scales to base 2
   const float c = a.scale_log2 * kUncode;
-  int in = 0, at = 0;  // stage the next tile goes to, stage the next tile comes from
-  int flying = 0;       // tiles issued and not yet used
+  uint32_t in = 0, at = 0;  // stages the next tile goes to and the next tile comes from, in bytes
+  int flying = 0;           // tiles issued and not yet used
   uint32_t row = warp * kTile;  // the next tile to issue: its row, and whether in the next piece
   bool next = false;
-  Cursor cursor{0, 0, false};
+  Cursor cursor{nullptr, nullptr, nullptr, 0};
+  const uint32_t mine = smem_u32(smem) + warp * kWarpBytes;
   int cur = 0;        // which of s_piece is this one
   enter(a, u);
   u.rows = static_cast<uint32_t>(left < u.n - u.off ? left : u.n - u.off);
@@ -352,13 +362,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       if (!next && row >= piece) {
         next = true;
         row = warp * kTile;
-        cursor.run = 0;
+        cursor.more = 0;
       }
       const Unit& from = s_piece[warp][next ? cur ^ 1 : cur];
       if (flying < (next ? kStages - 1 : kStages) && row < from.rows) {
-        load_tile(a, from, row, lane, cursor, smem_u32(mine) + in * kStageBytes,
-                  &s_absent[warp][in]);
-        in = in == kStages - 1 ? 0 : in + 1;
+        const uint32_t dst = mine + in + lane * 16;
+        if (cursor.more > 0) {
+          --cursor.more;
+          copy_tile(cursor, dst);
+        } else {
+          load_tile(a, from, row, lane, cursor, dst, &s_absent[warp][in / kStageBytes]);
+        }
+        in = in == (kStages - 1) * kStageBytes ? 0 : in + kStageBytes;
         row += kWarps * kTile;
         ++flying;
       }
@@ -414,19 +429,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
     for (uint32_t first = warp * kTile; first < piece; first += kWarps * kTile) {
       copies_wait<kStages - 1>();
       __syncwarp();  // every lane's copies
-      const uint8_t* kst = mine + at * kStageBytes;
-      const uint8_t* vst = kst + kTile * kQ4RowBytes;
-      const uint8_t* rec = vst + kTile * kQ4RowBytes;
-      uint32_t mask = piece - first >= kTile ? 0xffffffffu : (1u << (piece - first)) - 1u;
-      if (a.store.table) mask &= ~s_absent[warp][at];
-      at = at == kStages - 1 ? 0 : at + 1;
+      const uint8_t* stage = smem + warp * kWarpBytes + at;
+      const uint8_t* kst = stage + kr * kQ4RowBytes + 16 * t4;
+      const uint8_t* va = stage + (kTile + t4) * kQ4RowBytes + 8 * g8;
+      const uint8_t* vc = stage + (kTile + 4 + (t4 ^ 1)) * kQ4RowBytes + 8 * g8;
+      const uint8_t* rec = stage + 2 * kTile * kQ4RowBytes + kr * kQ4RecordBytes;
+      // rows that are there; all but where the piece ends or a block table entry is bad
+      uint32_t mask = 0xffffffffu;
+      if (piece - first < kTile) mask = (1u << (piece - first)) - 1u;
+      if (a.store.table) mask &= ~s_absent[warp][at / kStageBytes];
       // ---------------------------------------- scores of 2 x 16 rows
       float x[2][4];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
-        const int r0 = 16 * blk + kr, r1 = r0 + 8;
-        const uint4 w0 = *reinterpret_cast<const uint4*>(kst + r0 * kQ4RowBytes + 16 * t4);
-        const uint4 w1 = *reinterpret_cast<const uint4*>(kst + r1 * kQ4RowBytes + 16 * t4);
+        const int r0 = 16 * blk, r1 = r0 + 8;
+        const uint4 w0 = *reinterpret_cast<const uint4*>(kst + r0 * kQ4RowBytes);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(kst + r1 * kQ4RowBytes);
         const uint2 c0 = *reinterpret_cast<const uint2*>(rec + r0 * kQ4RecordBytes);
         const uint2 c1 = *reinterpret_cast<const uint2*>(rec + r1 * kQ4RecordBytes);
         float acc[2][4];
@@ -495,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       // ---------------------------------------- weights and values
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
-        const int r0 = 16 * blk + kr, r1 = r0 + 8;
+        const int r0 = 16 * blk, r1 = r0 + 8;
         const uint2 c0 = *reinterpret_cast<const uint2*>(rec + r0 * kQ4RecordBytes + 8);
         const uint2 c1 = *reinterpret_cast<const uint2*>(rec + r1 * kQ4RecordBytes + 8);
         float p[4];
@@ -504,12 +522,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         st.l[0] += p[0] + p[2];
         st.l[1] += p[1] + p[3];
         // this lane's V words: rows of the product's k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        const uint8_t* vb = vst + 16 * blk * kQ4RowBytes + 8 * g8;
-        const int va = t4, vc = 4 + (t4 ^ 1);
-        const uint2 v0 = *reinterpret_cast<const uint2*>(vb + va * kQ4RowBytes);
-        const uint2 v1 = *reinterpret_cast<const uint2*>(vb + vc * kQ4RowBytes);
-        const uint2 v2 = *reinterpret_cast<const uint2*>(vb + (va + 8) * kQ4RowBytes);
-        const uint2 v3 = *reinterpret_cast<const uint2*>(vb + (vc + 8) * kQ4RowBytes);
+        const uint2 v0 = *reinterpret_cast<const uint2*>(va + r0 * kQ4RowBytes);
+        const uint2 v1 = *reinterpret_cast<const uint2*>(vc + r0 * kQ4RowBytes);
+        const uint2 v2 = *reinterpret_cast<const uint2*>(va + r1 * kQ4RowBytes);
+        const uint2 v3 = *reinterpret_cast<const uint2*>(vc + r1 * kQ4RowBytes);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const uint32_t k0 = g ? c0.y : c0.x, k1 = g ? c1.y : c1.x;
@@ -536,14 +552,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         }
       }
       __syncwarp();  // every lane has read the stage
-      --flying;
-      issue();
+      if (cursor.more > 0 && !next) {
+        // the common case, with all stages in flight: the next tile goes where this one was
+        --cursor.more;
+        copy_tile(cursor, mine + at + lane * 16);
+        copies_commit();
+        row += kWarps * kTile;
+        in = at == (kStages - 1) * kStageBytes ? 0 : at + kStageBytes;
+      } else {
+        --flying;
+        issue();
+      }
+      at = at == (kStages - 1) * kStageBytes ? 0 : at + kStageBytes;
     }
 
     // ------------------------------------------------ combine the warps, write the piece
     // the stage to be filled next holds the warp's result now, [8 heads][128], then m[8], l[8], all
     // but m times 2^64; the other stages may hold the next piece's first tiles
-    float* res = reinterpret_cast<float*>(mine + in * kStageBytes);
+    float* res = reinterpret_cast<float*>(smem + warp * kWarpBytes + in);
     if (lane == 0) s_result[warp] = res;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
