@@ -39,15 +39,13 @@
 namespace ps {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 2;
+// Sixteen warps an SM either way (128 registers a thread): two blocks of eight, or one of sixteen.
+constexpr int kSmWarps = 16;
 constexpr int kTile = 32;  // rows of a warp's tile
 constexpr int kStages = 3;
 constexpr int kRowBytes = 2 * kQ4RowBytes + kQ4RecordBytes;
 constexpr int kStageBytes = kTile * kRowBytes;
 constexpr int kWarpBytes = kStages * kStageBytes;
-constexpr int kSmemBytes = kWarps * kWarpBytes;
 static_assert(kStageBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fits a stage");
 constexpr int kMinRowsPerBlock = 128;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -184,6 +182,7 @@ struct Cursor {
 };
 
 // Copies the tile at the cursor, 16 bytes a lane and load, and moves on to the warp's next.
+template <int kWarps>
 __device__ __forceinline__ void copy_tile(Cursor& c, uint32_t dst) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -198,6 +197,7 @@ __device__ __forceinline__ void copy_tile(Cursor& c, uint32_t dst) {
 
 // Copies the tile from row row0 of a piece into a stage (all lanes).  Rows past the piece's end
 // and rows that a bad block table entry leaves out become zeros; `absent` gets the latter.
+template <int kWarps>
 __device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, uint32_t row0,
                                           int lane, Cursor& c, uint32_t dst, uint32_t* absent) {
   const StoreArgs& st = a.store;
@@ -211,7 +211,7 @@ __device__ __forceinline__ void load_tile(const DecodeQ4Args& a, const Unit& u, 
     c.v = (f.ring ? st.v[1] : st.v[0]) + at;
     c.s = (f.ring ? st.s[1] : st.s[0]) + f.at * kQ4RecordBytes + lane * 16;
     c.more = static_cast<int32_t>((min(f.run, cnt) - kTile) / (kWarps * kTile));
-    copy_tile(c, dst);
+    copy_tile<kWarps>(c, dst);
     return;
   }
   // row by row: lane l copies a quarter of rows 8 j + l / 4, and row l's record
@@ -273,7 +273,9 @@ struct State {
 // come from fall into different halves of the shared memory banks.
 __device__ __forceinline__ int tile_row(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
 
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const DecodeQ4Args a) {
+template <int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
+    decode_q4_kernel(const DecodeQ4Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_absent[kWarps][kStages];
   __shared__ float* s_result[kWarps];
@@ -369,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
         const uint32_t dst = mine + in + lane * 16;
         if (cursor.more > 0) {
           --cursor.more;
-          copy_tile(cursor, dst);
+          copy_tile<kWarps>(cursor, dst);
         } else {
-          load_tile(a, from, row, lane, cursor, dst, &s_absent[warp][in / kStageBytes]);
+          load_tile<kWarps>(a, from, row, lane, cursor, dst, &s_absent[warp][in / kStageBytes]);
         }
         in = in == (kStages - 1) * kStageBytes ? 0 : in + kStageBytes;
         row += kWarps * kTile;
@@ -379,8 +381,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       }
       copies_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i) issue();
+    // the first tile and the query ahead of the rest: every block's first copies would otherwise
+    // queue behind 28 MB of everybody's third
+    issue();
 
     // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^64 (2^60
     // where the codes come out 16 times as large); and each group's sum of query dims
@@ -414,6 +417,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
 #pragma unroll
         for (int e = 0; e < 2; ++e) Q[g][e] = __shfl_sync(0xffffffffu, qs[g], 4 * (2 * t4 + e));
     }
+
+#pragma unroll 1
+    for (int i = 1; i < kStages; ++i) issue();
 
     State st;
     st.l[0] = st.l[1] = 0.f;
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
       if (cursor.more > 0 && !next) {
         // the common case, with all stages in flight: the next tile goes where this one was
         --cursor.more;
-        copy_tile(cursor, mine + at + lane * 16);
+        copy_tile<kWarps>(cursor, mine + at + lane * 16);
         copies_commit();
         row += kWarps * kTile;
         in = at == (kStages - 1) * kStageBytes ? 0 : at + kStageBytes;
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_q4_kernel(const
     }
     __syncthreads();
     {
-      const int head = warp;  // eight warps, eight heads; lane: dims 4 lane .. 4 lane + 3
+      const int head = warp;  // one warp a head; lane: dims 4 lane .. 4 lane + 3
       if (head < a.group) {
         float ml[kWarps], M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -711,61 +717,58 @@ __global__ void __launch_bounds__(128)
   if (a.lse && lane == 0) a.lse[bh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-int blocks_per_sm() {
-  static int cached[64] = {0};
+template <int kWarps>
+bool allow_smem() {
+  static bool done[64] = {false};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (cached[dev] == 0) {
-    int occ = 0;
-    if (cudaFuncSetAttribute(decode_q4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_q4_kernel, kThreads,
-                                                      kSmemBytes) != cudaSuccess ||
-        occ < 1)
-      occ = 1;
-    cached[dev] = occ < kBlocksPerSm ? occ : kBlocksPerSm;
-  }
-  return cached[dev];
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (!done[dev])
+    done[dev] = cudaFuncSetAttribute(decode_q4_kernel<kWarps>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kWarps * kWarpBytes) == cudaSuccess;
+  return done[dev];
 }
 
-// Blocks of the one-wave schedule, or 0 for one block a unit.
-int64_t share_grid(int64_t batch, int32_t hkv, int64_t max_keys) {
-  if (batch > kMaxBatch) return 0;
-  const int64_t units = batch * hkv;
-  const int64_t slots = (int64_t)sm_count() * blocks_per_sm();
-  if (units >= slots) return 0;
+// How a decode is laid out: blocks of `warps` warps, `grid` of them, sharing the rows or one a unit.
+struct Plan {
+  int64_t grid;
+  int warps;
+  bool share;
+};
+Plan plan_decode(int64_t batch, int32_t hkv, int64_t max_keys) {
+  const int64_t units = batch * hkv, sms = sm_count();
+  // two blocks an SM overlap one's start and end with the other's stream
+  if (units >= 2 * sms || batch > kMaxBatch) return {units, kSmWarps / 2, false};
+  if (units > sms) return {2 * sms, kSmWarps / 2, true};
+  // few units: one block an SM, a whole number of blocks a unit if that fills 5/6 of the SMs, so
+  // that equally long units split on their own borders
   int64_t g = units * ((max_keys + kMinRowsPerBlock - 1) / kMinRowsPerBlock);
-  if (g >= slots) {
-    g = slots;
-    // a multiple of the unit count that fills 5/6 of the slots: equally long units then split on
-    // their own borders, and no block changes unit midway
-    const int64_t even = units * (slots / units);
-    if (units <= slots && even * 6 >= slots * 5) g = even;
+  if (g >= sms) {
+    const int64_t even = units * (sms / units);
+    g = even * 6 >= sms * 5 ? even : sms;
   }
-  return g < 1 ? 1 : g;
+  if (g < 1) g = 1;
+  return {g, kSmWarps, g != units};
 }
 
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int64_t batch, int32_t hkv, int64_t max_keys) {
-  const int64_t g = share_grid(batch, hkv, max_keys);
-  if (g == 0 || batch == 0) return 0;
-  const size_t slots = size_t(2 * g) * kMaxGroup;
-  return slots * (kHeadDim + 1) * sizeof(float);
+  const Plan p = plan_decode(batch, hkv, max_keys);
+  if (!p.share || batch == 0) return 0;
+  return size_t(2 * p.grid) * kMaxGroup * (kHeadDim + 1) * sizeof(float);
 }
 
 int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream) {
-  const int64_t units = l.batch * l.hkv;
-  const int64_t g = share_grid(l.batch, l.hkv, (int64_t)l.store.lp + l.store.w);
-  const int64_t grid = g ? g : units;
-  if (grid > 0x7fffffff) return fail(PS_ERR_UNSUPPORTED, "decode grid too large");
+  const Plan p = plan_decode(l.batch, l.hkv, (int64_t)l.store.lp + l.store.w);
+  if (p.grid > 0x7fffffff) return fail(PS_ERR_UNSUPPORTED, "decode grid too large");
   DecodeQ4Args a;
   a.q = static_cast<const __nv_bfloat16*>(l.q);
   a.pos = l.pos;
   a.out = static_cast<__nv_bfloat16*>(l.out);
   a.lse = l.lse;
-  a.ws_o = g ? static_cast<float*>(l.workspace) : nullptr;
-  a.ws_lse = g ? a.ws_o + size_t(2 * g) * kMaxGroup * kHeadDim : nullptr;
+  a.ws_o = p.share ? static_cast<float*>(l.workspace) : nullptr;
+  a.ws_lse = p.share ? a.ws_o + size_t(2 * p.grid) * kMaxGroup * kHeadDim : nullptr;
   a.status = l.status;
   a.batch = static_cast<int32_t>(l.batch);
   a.hq = l.hq;
@@ -773,13 +776,18 @@ int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream) {
   a.group = l.hq / l.hkv;
   a.scale_log2 = l.scale * kLog2e;
   a.store = l.store;
-  PS_TRY(check_cuda(launch_pdl(decode_q4_kernel, dim3(static_cast<unsigned>(grid)),
-                               dim3(kThreads), kSmemBytes, stream, a),
-                    "decode_q4_kernel launch"));
-  if (!g) return PS_OK;
+  const bool one = p.warps == kSmWarps;
+  if (!(one ? allow_smem<kSmWarps>() : allow_smem<kSmWarps / 2>()))
+    return fail(PS_ERR_CUDA, "decode_q4_kernel: shared memory refused");
+  PS_TRY(check_cuda(
+      launch_pdl(one ? decode_q4_kernel<kSmWarps> : decode_q4_kernel<kSmWarps / 2>,
+                 dim3(static_cast<unsigned>(p.grid)), dim3(p.warps * 32), p.warps * kWarpBytes,
+                 stream, a),
+      "decode_q4_kernel launch"));
+  if (!p.share) return PS_OK;
   return check_cuda(
       launch_pdl(merge_q4_kernel, dim3(static_cast<unsigned>((l.batch * l.hq + 3) / 4)), dim3(128),
-                 0, stream, a, static_cast<int32_t>(g)),
+                 0, stream, a, static_cast<int32_t>(p.grid)),
       "merge_q4_kernel launch");
 }
 
