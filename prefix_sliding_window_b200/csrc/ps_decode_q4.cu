@@ -259,8 +259,22 @@ __device__ __forceinline__ uint32_t pair_byte(uint32_t w) { return w & 0x00ff00f
 __device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
 __device__ __forceinline__ uint32_t pair_byte1(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The halves of a word of two bf16 as floats: adding -0 in mixed precision, which the FMA pipe
+// does, where a shift or a mask would take the integer pipe that the codes are unpacked on.
+__device__ __forceinline__ float lo_f(uint32_t w) {
+  float y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, 0f80000000;\n\t}"
+      : "=f"(y)
+      : "r"(w));
+  return y;
+}
+__device__ __forceinline__ float hi_f(uint32_t w) {
+  float y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, h, 0f80000000;\n\t}"
+      : "=f"(y)
+      : "r"(w));
+  return y;
+}
 
 // One warp's running softmax and accumulators over the heads (2 t, 2 t + 1) of its lane's t.
 struct State {
@@ -381,27 +395,32 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
       }
       copies_commit();
     };
-    // the first tile and the query ahead of the rest: every block's first copies would otherwise
-    // queue behind 28 MB of everybody's third
-    issue();
-
     // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^64 (2^60
     // where the codes come out 16 times as large); and each group's sum of query dims
     uint32_t qf[2][2][4];
     float Q[2][2];  // of heads 2 t + e, on the products' scale
     {
       const int head0 = s_piece[warp][cur].b * a.hq + s_piece[warp][cur].h * a.group;
+      uint4 w[2][2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          w[g][j] = make_uint4(0, 0, 0, 0);
+          if (g8 < a.group)
+            w[g][j] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(head0 + g8) * kHeadDim +
+                                                      64 * g + 16 * t4 + 8 * j);
+        }
+      // the query, then every block's first tile, then the rest: behind 28 MB of everybody's
+      // third tiles the query would arrive 5 us later
+      issue();
       float qs[2];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         qs[g] = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (g8 < a.group)
-            w = *reinterpret_cast<const uint4*>(a.q + (int64_t)(head0 + g8) * kHeadDim + 64 * g +
-                                                16 * t4 + 8 * j);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t ww[4] = {w[g][j].x, w[g][j].y, w[g][j].z, w[g][j].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f = (i & 1) ? kLift / 16.f : kLift;
@@ -604,43 +623,40 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
       }
     }
     __syncthreads();
-    {
-      const int head = warp;  // one warp a head; lane: dims 4 lane .. 4 lane + 3
-      if (head < a.group) {
-        float ml[kWarps], M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = s_result[w][kMaxGroup * kHeadDim + head];
-          M = fmaxf(M, ml[w]);
-        }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float* r = s_result[w];
-          const float f = ml[w] == -INFINITY ? 0.f : fast_exp2(ml[w] - M);
-          const float lw = r[kMaxGroup * kHeadDim + kMaxGroup + head];
-          if (lw == 0.f) continue;  // no row of this warp counted
-          const float4 y = reinterpret_cast<const float4*>(r + head * kHeadDim)[lane];
-          L = fmaf(f, lw, L);
-          acc.x = fmaf(f, y.x, acc.x);
-          acc.y = fmaf(f, y.y, acc.y);
-          acc.z = fmaf(f, y.z, acc.z);
-          acc.w = fmaf(f, y.w, acc.w);
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float lse2 = L == 0.f ? -INFINITY : M + log2f(L * (1.f / kLift));
-        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-        if (piece < s_piece[warp][cur].n) {
-          const int64_t slot = (2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1)) * kMaxGroup + head;
-          reinterpret_cast<float4*>(a.ws_o + slot * kHeadDim)[lane] = acc;
-          if (lane == 0) a.ws_lse[slot] = lse2;
-        } else {
-          const int64_t row = (int64_t)s_piece[warp][cur].b * a.hq +
-                              s_piece[warp][cur].h * a.group + head;
-          reinterpret_cast<uint2*>(a.out + row * kHeadDim)[lane] =
-              make_uint2(cvt_bf16x2(acc.x, acc.y), cvt_bf16x2(acc.z, acc.w));
-          if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
-        }
+    // one warp a head, dims 4 lane .. 4 lane + 3.  (Spread over all sixteen warps and unrolled it
+    // took half a microsecond longer: this runs once a piece, from a cold instruction cache.)
+    if (warp < a.group) {
+      const int head = warp;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w)
+        M = fmaxf(M, s_result[w][kMaxGroup * kHeadDim + head]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w) {
+        const float* r = s_result[w];
+        const float m = r[kMaxGroup * kHeadDim + head];
+        const float f = m == -INFINITY ? 0.f : fast_exp2(m - M);  // (such a warp left zeros)
+        const float4 y = reinterpret_cast<const float4*>(r + head * kHeadDim)[lane];
+        L = fmaf(f, r[kMaxGroup * kHeadDim + kMaxGroup + head], L);
+        acc.x = fmaf(f, y.x, acc.x);
+        acc.y = fmaf(f, y.y, acc.y);
+        acc.z = fmaf(f, y.z, acc.z);
+        acc.w = fmaf(f, y.w, acc.w);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float lse2 = L == 0.f ? -INFINITY : M + log2f(L * (1.f / kLift));
+      acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+      if (piece < s_piece[warp][cur].n) {
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1)) * kMaxGroup + head;
+        reinterpret_cast<float4*>(a.ws_o + slot * kHeadDim)[lane] = acc;
+        if (lane == 0) a.ws_lse[slot] = lse2;
+      } else {
+        const int64_t row = (int64_t)s_piece[warp][cur].b * a.hq +
+                            s_piece[warp][cur].h * a.group + head;
+        reinterpret_cast<uint2*>(a.out + row * kHeadDim)[lane] =
+            make_uint2(cvt_bf16x2(acc.x, acc.y), cvt_bf16x2(acc.z, acc.w));
+        if (a.lse && lane == 0) a.lse[row] = lse2 * kLn2;
       }
     }
     if (left <= 0) break;
