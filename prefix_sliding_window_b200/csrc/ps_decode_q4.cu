@@ -47,7 +47,9 @@ constexpr int kRowBytes = 2 * kQ4RowBytes + kQ4RecordBytes;
 constexpr int kStageBytes = kTile * kRowBytes;
 constexpr int kWarpBytes = kStages * kStageBytes;
 static_assert(kStageBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fits a stage");
-constexpr int kMinRowsPerBlock = 128;
+// Rows of a block where a few units are split further than the SMs ask for: a tile a warp.  (One
+// sequence of 4196 rows: 128 rows a block 12.7 us, 256 11.0, 512 10.9.)
+constexpr int kMinRowsPerBlock = kSmWarps * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxBatch = 1024;
@@ -666,17 +668,21 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
   }
 }
 
-// Combines the pieces of one (sequence, query head), one warp each, where its unit was split:
+// Combines the pieces of one (sequence, query head), one block each, where its unit was split:
 // block c of the decode owned the rows [total c / grid, total (c + 1) / grid), so which blocks hold
 // pieces follows from the positions alone.  A unit's later pieces are their blocks' first ones, its
-// earliest is its block's first or last.  Lane i owns dims 4 i .. 4 i + 3.
-__global__ void __launch_bounds__(128)
+// earliest is its block's first or last.  Each warp takes every fourth piece, eight in flight (a
+// long row has dozens, and each round is a trip to L2: four cost 1.5 us more at 33 pieces); lane i
+// owns dims 4 i .. 4 i + 3.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeBatch = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32)
     merge_q4_kernel(const DecodeQ4Args a, int32_t grid) {
-  const int lane = threadIdx.x & 31;
-  const int64_t bh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const bool live = bh < (int64_t)a.batch * a.hq;
-  const int b = live ? static_cast<int>(bh / a.hq) : 0;
-  const int head = live ? static_cast<int>(bh % a.hq) : 0;
+  __shared__ float4 s_acc[kMergeWarps][32];
+  __shared__ float2 s_ml[kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t bh = blockIdx.x;
+  const int b = static_cast<int>(bh / a.hq), head = static_cast<int>(bh % a.hq);
   const int h = head / a.group, hh = head % a.group;
   const RowScan sc = scan_rows(a, lane, false);
   const int64_t total = sc.total * a.hkv;
@@ -693,15 +699,16 @@ __global__ void __launch_bounds__(128)
   }
   pdl_trigger();
   pdl_wait();
-  if (!live || (n > 0 && c_lo == c_hi)) return;  // a whole unit is written already
+  if (n > 0 && c_lo == c_hi) return;  // a whole unit is written already
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, L = 0.f;
-  for (int c0 = c_lo; c0 <= c_hi; c0 += 4) {
-    float lv[4];
-    float4 ov[4];
+  for (int c0 = c_lo + warp; c0 <= c_hi; c0 += kMergeWarps * kMergeBatch) {
+    float lv[kMergeBatch];
+    float4 ov[kMergeBatch];
+    float Mn = M;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k;
+    for (int k = 0; k < kMergeBatch; ++k) {
+      const int c = c0 + k * kMergeWarps;
       lv[k] = -INFINITY;
       ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       // with fewer rows than blocks some blocks own none and wrote no piece
@@ -711,13 +718,14 @@ __global__ void __launch_bounds__(128)
         ov[k] = reinterpret_cast<const float4*>(a.ws_o + slot * kHeadDim)[lane];
       }
     }
-    const float Mn = fmaxf(M, fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3])));
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) Mn = fmaxf(Mn, lv[k]);
     const float ref = Mn == -INFINITY ? 0.f : Mn;
     const float f = fast_exp2(M - ref);
     L *= f;
     acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kMergeBatch; ++k) {
       const float e = fast_exp2(lv[k] - ref);
       L += e;
       acc.x = fmaf(e, ov[k].x, acc.x);
@@ -725,6 +733,23 @@ __global__ void __launch_bounds__(128)
       acc.z = fmaf(e, ov[k].z, acc.z);
       acc.w = fmaf(e, ov[k].w, acc.w);
     }
+    M = Mn;
+  }
+  s_acc[warp][lane] = acc;
+  if (lane == 0) s_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const float2 ml = s_ml[w];
+    const float4 y = s_acc[w][lane];
+    const float Mn = fmaxf(M, ml.x), ref = Mn == -INFINITY ? 0.f : Mn;
+    const float f = fast_exp2(M - ref), e = fast_exp2(ml.x - ref);
+    L = L * f + ml.y * e;
+    acc.x = acc.x * f + y.x * e;
+    acc.y = acc.y * f + y.y * e;
+    acc.z = acc.z * f + y.z * e;
+    acc.w = acc.w * f + y.w * e;
     M = Mn;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -802,8 +827,8 @@ int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream) {
       "decode_q4_kernel launch"));
   if (!p.share) return PS_OK;
   return check_cuda(
-      launch_pdl(merge_q4_kernel, dim3(static_cast<unsigned>((l.batch * l.hq + 3) / 4)), dim3(128),
-                 0, stream, a, static_cast<int32_t>(p.grid)),
+      launch_pdl(merge_q4_kernel, dim3(static_cast<unsigned>(l.batch * l.hq)),
+                 dim3(kMergeWarps * 32), 0, stream, a, static_cast<int32_t>(p.grid)),
       "merge_q4_kernel launch");
 }
 
