@@ -7,6 +7,9 @@
 // decode step's single tokens.  Of tokens that share a ring slot only the newest of the call is
 // written, so the result does not depend on which block runs first.
 //
+// A warp keeps a token's angles and weights in registers over all of its heads, as in the pass
+// without a store; with few tokens eight warps share one.
+//
 // 4-bit rows: eight lanes hold a row, so the least and greatest value of a group of 64 dims take
 // three shuffles each; every lane packs its two 8-dim chunks into two of the row's sixteen words.
 #include <cuda_bf16.h>
@@ -20,61 +23,89 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Least and greatest of two or of a row's eight lanes; a NaN stays one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float row_min(float v) {
-  v = fminf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = fminf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  return fminf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = min_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = min_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  return min_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
 }
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  return max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
 }
 
-// Quantises a row held by eight lanes (chunks p.c1, p.c2 of a lane: x[0..7], x[8..15], on the
-// bf16 grid) and writes it: payload words at `pay`, (s, m) of both groups at `rec` (8 bytes).
-// All lanes take part; only `live` ones write.
-__device__ __forceinline__ void quantise_row(const RopeLane& p, const float (&x)[16], bool live,
-                                             int lane8, uint8_t* pay, uint8_t* rec) {
-  // least and greatest of each group; a value that is not finite makes the spread a NaN
-  float lo[2], hi[2], odd[2];
+// Quantises a row held by eight lanes (chunks p.c1, p.c2 of a lane, bf16) and writes it: payload
+// words at `pay`, (s, m) of both groups at `rec` (8 bytes).  All lanes take part; only `live` ones
+// write.  A code is the rounded quotient (x - m) / s; the product with 1 / s is within 2e-6 of it,
+// so only a product that near to a half needs the division.
+__device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1, const uint4& r2,
+                                             bool live, int lane8, uint8_t* pay, uint8_t* rec) {
+  float x[2][8], lo[2], hi[2];
+  const uint32_t w[2][4] = {{r1.x, r1.y, r1.z, r1.w}, {r2.x, r2.y, r2.z, r2.w}};
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    lo[c] = hi[c] = x[8 * c];
-    odd[c] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo[c] = fminf(lo[c], x[8 * c + e]);
-      hi[c] = fmaxf(hi[c], x[8 * c + e]);
-      odd[c] = fmaf(x[8 * c + e], 0.f, odd[c]);  // 0, or NaN
+    for (int i = 0; i < 4; ++i) {
+      x[c][2 * i] = __uint_as_float(w[c][i] << 16);
+      x[c][2 * i + 1] = __uint_as_float(w[c][i] & 0xffff0000u);
+    }
+    lo[c] = hi[c] = x[c][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+      lo[c] = min_nan(lo[c], x[c][e]);
+      hi[c] = max_nan(hi[c], x[c][e]);
     }
   }
   const int g1 = p.c1 >> 3, g2 = p.c2 >> 3;
   float m[2], s[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float a = fminf(g1 == g ? lo[0] : INFINITY, g2 == g ? lo[1] : INFINITY);
-    const float b = fmaxf(g1 == g ? hi[0] : -INFINITY, g2 == g ? hi[1] : -INFINITY);
-    const float least = row_min(a), most = row_max(b);
-    const float o = (g1 == g ? odd[0] : 0.f) + (g2 == g ? odd[1] : 0.f);
-    const bool bad = row_max(o != o ? 1.f : 0.f) > 0.f;
-    const float sc = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(most - least, 15.f)));
-    m[g] = least;
-    s[g] = sc;
-    if (bad || !(sc < INFINITY)) m[g] = s[g] = __uint_as_float(0x7fc00000u);
+    m[g] = row_min(min_nan(g1 == g ? lo[0] : INFINITY, g2 == g ? lo[1] : INFINITY));
+    const float most =
+        row_max(max_nan(g1 == g ? hi[0] : -INFINITY, g2 == g ? hi[1] : -INFINITY));
+    s[g] = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(most - m[g], 15.f)));
+    if (!(s[g] < INFINITY)) m[g] = s[g] = __uint_as_float(0x7fc00000u);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int chunk = c ? p.c2 : p.c1;
     const int g = chunk >> 3, b = chunk & 7;
     const float mm = g ? m[1] : m[0], ss = g ? s[1] : s[0];
-    uint32_t word = 0;
+    const float inv = __fdiv_rn(1.f, ss);
+    float u[8];
+    bool sure = true;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float u = ss > 0.f ? rintf(__fdiv_rn(x[8 * c + e] - mm, ss)) : 0.f;
-      u = fminf(fmaxf(u, 0.f), 15.f);
-      word |= static_cast<uint32_t>(u) << (4 * (e >> 1) + 16 * (e & 1));
+      const float t = (x[c][e] - mm) * inv;
+      u[e] = rintf(t);
+      sure = sure && fabsf(t - u[e]) < 0.499996f;
     }
+    if (!sure) {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const float q = ss > 0.f ? rintf(__fdiv_rn(x[c][e] - mm, ss)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i == e) u[i] = q;
+      }
+    }
+    // halves of the word as sums of codes times 16^i, exact in fp32
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = fminf(u[e], 15.f);
+    const float lo16 = fmaf(u[6], 4096.f, fmaf(u[4], 256.f, fmaf(u[2], 16.f, u[0])));
+    const float hi16 = fmaf(u[7], 4096.f, fmaf(u[5], 256.f, fmaf(u[3], 16.f, u[1])));
+    const uint32_t word = static_cast<uint32_t>(lo16) | (static_cast<uint32_t>(hi16) << 16);
     if (live) *reinterpret_cast<uint32_t*>(pay + 4 * (2 * b + g)) = word;
   }
   if (live && lane8 == 0)
@@ -82,98 +113,92 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const float (&x)
         make_uint2(cvt_bf16x2(s[0], m[0]), cvt_bf16x2(s[1], m[1]));
 }
 
-__device__ __forceinline__ void round_bf16(float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t w = cvt_bf16x2(x[2 * i], x[2 * i + 1]);
-    x[2 * i] = __uint_as_float(w << 16);
-    x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-  }
-}
+constexpr int kTokens = 2;  // consecutive tokens of a warp, where there are tokens enough
 
-// One block per TT tokens of the call.
-template <int TT, bool Q4>
-__global__ void __launch_bounds__(kThreads) append_norm_kernel(const AppendNormArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ __align__(16) float s_cos[TT][kHalfDim];
-  __shared__ __align__(16) float s_sin[TT][kHalfDim];
+// SPLIT warps share a token (1 or 8).
+template <int SPLIT, bool Q4, bool INTER>
+__global__ void __launch_bounds__(kThreads, Q4 ? 2 : 3)
+    append_norm_kernel(const AppendNormArgs a) {
+  __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
+  __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tokens = a.batch * a.T;
-  const int64_t tok0 = (int64_t)blockIdx.x * TT;
-  const int ntok = static_cast<int>(tokens - tok0 < TT ? tokens - tok0 : TT);
-  const RopeLane p = rope_lane(a.rope, lane & 7);
+  const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
   const int nq = a.q ? (a.hq + 3) / 4 : 0;
   const int nk = (a.hkv + 3) / 4;
-  const int per = nq + 2 * nk;
-
-  for (int i = threadIdx.x; i < ntok * (a.rope.dim / 2); i += kThreads) {
-    const int t = i / (a.rope.dim / 2), f = i % (a.rope.dim / 2);
-    const int64_t tok = tok0 + t;
-    const int64_t pos = a.pos0[tok / a.T] + tok % a.T;
-    if (!bad_rope_position(pos)) rope_angle(a.rope, pos, f, s_cos[t], s_sin[t]);
-  }
+  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
+  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
+  int64_t tok = SPLIT == 1 ? gw * kTokens : gw / SPLIT;
+  int64_t end = tok + (SPLIT == 1 ? kTokens : 1);
+  if (end > a.batch * a.T) end = a.batch * a.T;
+  pdl_wait();
+  pdl_trigger();
   load_norm_weights(a.norm, s_w);
   __syncthreads();
 
-  for (int it = warp; it < ntok * per; it += kWarps) {
-    const int t = it / per;
-    int sub = it % per;
-    const int64_t tok = tok0 + t, b = tok / a.T;
-    const int64_t p0 = a.pos0[b];
-    const int64_t pos = p0 + tok % a.T;
-    const bool is_q = sub < nq;
-    const bool is_v = !is_q && sub >= nq + nk;
-    if (!is_q) sub -= is_v ? nq + nk : nq;
-    const int head = 4 * sub + (lane >> 3);
-    const int heads = is_q ? a.hq : a.hkv;
-    StoreRow row = store_row(a.store, a.hkv, b, pos);
+  for (; tok < end; ++tok) {
+    const int64_t b = tok / a.T;
+    const int64_t p0 = a.pos0[b], pos = p0 + (tok - b * a.T);
+    const StoreRow row = store_row(a.store, a.hkv, b, pos);
+    if (row.flag && sub0 == 0 && a.status && lane == 0) atomicOr(a.status, row.flag);
     // a token the store has no place for is skipped; its queries become zeros.  A bad table
-    // entry only loses the row
-    const bool skip = bad_rope_position(pos) || (row.flag && !a.store.table);
-    if (row.flag && a.status && it % per == nq && lane == 0) atomicOr(a.status, row.flag);
-    if (!is_q) {
-      // a newer token of this call owns the ring slot
-      const bool stale = pos >= a.store.lp && pos <= p0 + a.T - 1 - a.store.w;
-      if (row.flag || (stale && !a.store.linear)) continue;
-    }
-    bool live = head < heads;
-    const __nv_bfloat16* src = (is_q ? a.q + tok * a.q_stride
-                                     : is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) +
-                               head * kHeadDim;
-    uint4 v1 = make_uint4(0, 0, 0, 0), v2 = v1;
-    if (live) {
-      v1 = *reinterpret_cast<const uint4*>(src + 8 * p.c1);
-      v2 = *reinterpret_cast<const uint4*>(src + 8 * p.c2);
-    }
-    const int64_t at = row.unit + head * row.stride;
-    float x[16];
-    if (!is_v || Q4) {
-      unpack8(v1, x);
-      unpack8(v2, x + 8);
-    }
-    if (!is_v) {
-      norm_and_turn(a.rope, p, (is_q ? a.norm.wq : a.norm.wk) != nullptr,
-                    s_w + (is_q ? 0 : kHeadDim), a.norm.eps, s_cos[t], s_sin[t], x);
-      v1 = pack8(x);
-      v2 = pack8(x + 8);
-    }
-    if (Q4 && !is_q) {
-      if (!is_v) round_bf16(x);
-      uint8_t* pay = (is_v ? a.store.v[row.ring] : a.store.k[row.ring]) + at * kQ4RowBytes;
-      uint8_t* rec = a.store.s[row.ring] + at * kQ4RecordBytes + (is_v ? 8 : 0);
-      quantise_row(p, x, live, lane & 7, pay, rec);
-      continue;
-    }
-    __nv_bfloat16* dst =
-        is_q ? a.q_out + (tok * a.hq + head) * kHeadDim
-             : reinterpret_cast<__nv_bfloat16*>(is_v ? a.store.v[row.ring] : a.store.k[row.ring]) +
-                   at * kHeadDim;
-    if (is_q && skip) v1 = v2 = make_uint4(0, 0, 0, 0);
-    if (live) {
-      *reinterpret_cast<uint4*>(dst + 8 * p.c1) = v1;
-      *reinterpret_cast<uint4*>(dst + 8 * p.c2) = v2;
+    // entry only loses the row.  A row whose ring slot a newer token of the call owns is not written
+    const bool bad = bad_rope_position(pos);
+    const bool skip = bad || (row.flag && !a.store.table);
+    const bool stale =
+        !a.store.linear && pos >= a.store.lp && pos <= p0 + a.T - 1 - a.store.w;
+    const int per = nq + (row.flag || stale ? 0 : 2 * nk);
+
+    auto load = [&](int sub, uint4& r1, uint4& r2) {
+      r1 = r2 = make_uint4(0, 0, 0, 0);
+      if (sub >= per) return;
+      const bool is_q = sub < nq, is_v = sub >= nq + nk;
+      const int head = 4 * (is_q ? sub : is_v ? sub - nq - nk : sub - nq) + (lane >> 3);
+      if (head >= (is_q ? a.hq : a.hkv)) return;
+      const __nv_bfloat16* src = (is_q ? a.q + tok * a.q_stride
+                                       : is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) +
+                                 head * kHeadDim;
+      r1 = *reinterpret_cast<const uint4*>(src + 8 * p.c1);
+      r2 = *reinterpret_cast<const uint4*>(src + 8 * p.c2);
+    };
+    uint4 n1, n2;
+    load(sub0, n1, n2);
+    if (sub0 < per) rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+    RowCoef coef;
+    int side = -1;  // whose weights are in coef
+    for (int sub = sub0; sub < per; sub += SPLIT) {
+      uint4 r1 = n1, r2 = n2;
+      load(sub + SPLIT, n1, n2);
+      const bool is_q = sub < nq, is_v = sub >= nq + nk;
+      const int head = 4 * (is_q ? sub : is_v ? sub - nq - nk : sub - nq) + (lane >> 3);
+      const bool live = head < (is_q ? a.hq : a.hkv);
+      if (!is_v) {
+        const bool norm = (is_q ? a.norm.wq : a.norm.wk) != nullptr;
+        if (side != is_q) {
+          side = is_q;
+          row_coef<INTER>(p, norm, s_w + (is_q ? 0 : kHeadDim), s_cos[warp], s_sin[warp], coef);
+        }
+        float u[8], v[8];
+        unpack_pairs<INTER>(r1, r2, u, v);
+        norm_and_turn(p, norm, coef, a.norm.eps, u, v);
+        pack_pairs<INTER>(u, v, r1, r2);
+        if (is_q && skip) r1 = r2 = make_uint4(0, 0, 0, 0);
+      }
+      const int64_t at = row.unit + head * row.stride;
+      if (Q4 && !is_q) {
+        uint8_t* pay = (is_v ? a.store.v[row.ring] : a.store.k[row.ring]) + at * kQ4RowBytes;
+        uint8_t* rec = a.store.s[row.ring] + at * kQ4RecordBytes + (is_v ? 8 : 0);
+        quantise_row(p, r1, r2, live, lane & 7, pay, rec);
+        continue;
+      }
+      __nv_bfloat16* dst =
+          is_q ? a.q_out + (tok * a.hq + head) * kHeadDim
+               : reinterpret_cast<__nv_bfloat16*>(is_v ? a.store.v[row.ring]
+                                                       : a.store.k[row.ring]) + at * kHeadDim;
+      if (live) {
+        *reinterpret_cast<uint4*>(dst + 8 * p.c1) = r1;
+        *reinterpret_cast<uint4*>(dst + 8 * p.c2) = r2;
+      }
     }
   }
 }
@@ -211,7 +236,8 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           x[e] = fmaf(s, static_cast<float>((w >> (4 * (e >> 1) + 16 * (e & 1))) & 15u), m);
-        y[g] = pack8(x);
+        y[g] = make_uint4(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]), cvt_bf16x2(x[4], x[5]),
+                          cvt_bf16x2(x[6], x[7]));
       }
     }
     __nv_bfloat16* dst = out + i * kHeadDim + 8 * lane8;
@@ -222,15 +248,21 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
 
 }  // namespace
 
+template <bool INTER>
+static auto pick_append(bool split, bool q4) {
+  return q4 ? (split ? append_norm_kernel<kWarps, true, INTER> : append_norm_kernel<1, true, INTER>)
+            : (split ? append_norm_kernel<kWarps, false, INTER>
+                     : append_norm_kernel<1, false, INTER>);
+}
+
 int launch_append_norm(const AppendNormArgs& a, bool q4, cudaStream_t stream) {
   const int64_t tokens = a.batch * a.T;
   if (tokens <= 0) return PS_OK;
-  // four tokens a block share the set-up once there are blocks enough for every SM
-  const bool wide = tokens > 8 * (int64_t)sm_count();
-  const int64_t grid = wide ? (tokens + 3) / 4 : tokens;
+  const bool split = tokens < 16 * (int64_t)sm_count();  // fewer than one a warp slot
+  const int64_t grid = split ? tokens : (tokens + kWarps * kTokens - 1) / (kWarps * kTokens);
   if (grid > 0x7fffffff) return fail(PS_ERR_UNSUPPORTED, "too many tokens");
-  auto kern = q4 ? (wide ? append_norm_kernel<4, true> : append_norm_kernel<1, true>)
-                 : (wide ? append_norm_kernel<4, false> : append_norm_kernel<1, false>);
+  auto kern = pick_append<false>(split, q4);
+  if (a.rope.interleaved) kern = pick_append<true>(split, q4);
   return check_cuda(
       launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a),
       "append_norm_kernel launch");

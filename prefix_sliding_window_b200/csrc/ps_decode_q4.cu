@@ -160,22 +160,6 @@ __device__ __forceinline__ Rows locate(const DecodeQ4Args& a, const Unit& u, uin
   return r;
 }
 
-// 16 bytes to shared memory, asynchronously; zeros where !there (src is not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_if(uint32_t dst, const uint8_t* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the latest N groups of this thread's copies have landed.
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A lane's place in a piece: where its 16 bytes of the warp's next tile are, if that is one of
 // `more` tiles that follow in the same run of rows.
 struct Cursor {
@@ -758,18 +742,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (a.lse && lane == 0) a.lse[bh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int kWarps>
-bool allow_smem() {
-  static bool done[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  if (!done[dev])
-    done[dev] = cudaFuncSetAttribute(decode_q4_kernel<kWarps>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kWarps * kWarpBytes) == cudaSuccess;
-  return done[dev];
-}
-
 // How a decode is laid out: blocks of `warps` warps, `grid` of them, sharing the rows or one a unit.
 struct Plan {
   int64_t grid;
@@ -818,12 +790,12 @@ int launch_decode_q4(const DecodeQ4Launch& l, cudaStream_t stream) {
   a.scale_log2 = l.scale * kLog2e;
   a.store = l.store;
   const bool one = p.warps == kSmWarps;
-  if (!(one ? allow_smem<kSmWarps>() : allow_smem<kSmWarps / 2>()))
-    return fail(PS_ERR_CUDA, "decode_q4_kernel: shared memory refused");
+  const size_t smem = size_t(p.warps) * kWarpBytes;
+  PS_TRY(one ? allow_smem<decode_q4_kernel<kSmWarps>>(smem)
+             : allow_smem<decode_q4_kernel<kSmWarps / 2>>(smem));
   PS_TRY(check_cuda(
       launch_pdl(one ? decode_q4_kernel<kSmWarps> : decode_q4_kernel<kSmWarps / 2>,
-                 dim3(static_cast<unsigned>(p.grid)), dim3(p.warps * 32), p.warps * kWarpBytes,
-                 stream, a),
+                 dim3(static_cast<unsigned>(p.grid)), dim3(p.warps * 32), smem, stream, a),
       "decode_q4_kernel launch"));
   if (!p.share) return PS_OK;
   return check_cuda(

@@ -406,6 +406,26 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
 
 namespace ps {
 
+// ------------------------------------------------ asynchronous 16-byte copies
+// 16 bytes from global to shared memory; the _if form writes zeros where !there (and reads
+// nothing).  Copies are waited for by groups, each thread for its own.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the latest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------ programmatic dependent launch
 // A kernel launched with programmatic stream serialization may start before the previous
 // kernel in the stream has finished; pdl_wait() blocks until that kernel has completed and

@@ -67,6 +67,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // Streaming multiprocessor count of the current device.
 int sm_count();
 
+// Lets `Kernel` take `bytes` of dynamic shared memory, asking the runtime once a device.
+template <auto Kernel>
+int allow_smem(size_t bytes) {
+  static bool done[64] = {false};
+  int dev = 0;
+  const int rc = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != PS_OK) return rc;
+  if (dev >= 0 && dev < 64 && done[dev]) return PS_OK;
+  const int set = check_cuda(
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+      "cudaFuncSetAttribute");
+  if (set == PS_OK && dev >= 0 && dev < 64) done[dev] = true;
+  return set;
+}
+
 // ---------------------------------------------------------------- append
 struct AppendArgs {
   const void* k_new;

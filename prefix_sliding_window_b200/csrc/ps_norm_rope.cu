@@ -3,8 +3,11 @@
 //   forward:  y = R(p) (x rstd w),  rstd = 1 / sqrt(mean x^2 + eps)
 //   backward: g = R(p)^T dy,  n = x rstd,  dw = sum g n,  dx = rstd (w g - n mean(w g n))
 // Both stream every row once (forward one read and one write of each bf16 row, backward two
-// reads and one write) and are bound by HBM; the arithmetic is a few fp32 operations an element
-// and the token's angles, formed once per token in float64 and shared by all its heads.
+// reads and one write) and are bound by HBM.  A warp keeps a token's angles and weights in
+// registers over all of its heads; the rows of the next items are in flight as asynchronous copies
+// into a ring of shared memory, every lane its own 16-byte chunks, so that the depth of the
+// prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
+// 28 + 4 heads, XXX with the ring).  With few tokens eight warps share one.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -14,185 +17,264 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 3, kAhead = 5;  // items in flight a warp, forward
+constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 3;  // backward: an item is twice the bytes
 
-// One item: four heads of one token's q or k.
-struct Item {
-  const __nv_bfloat16* src;
-  __nv_bfloat16* dst;
-  bool is_k, live;  // live: this lane's head exists
-};
-
-// One block handles TT tokens.
-template <int TT>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ __align__(16) float s_cos[TT][kHalfDim];
-  __shared__ __align__(16) float s_sin[TT][kHalfDim];
+// Warps stride over tokens; SPLIT of them share one (1 or 8) and take its items in turn.
+template <int SPLIT, bool INTER>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const NormRopeArgs a) {
+  extern __shared__ __align__(16) uint4 s_all[];  // [kWarps][kAhead + 1][2][32]
+  uint4 (*s_ring)[kAhead + 1][2][32] = reinterpret_cast<uint4 (*)[kAhead + 1][2][32]>(s_all);
+  __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
+  __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tok0 = (int64_t)blockIdx.x * TT;
-  const int ntok = static_cast<int>(a.n - tok0 < TT ? a.n - tok0 : TT);
-  const RopeLane p = rope_lane(a.rope, lane & 7);
+  const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
   const int nq = a.q ? (a.hq + 3) / 4 : 0;
-  const int nk = a.k ? (a.hkv + 3) / 4 : 0;
-  const int per = nq + nk;
+  const int per = nq + (a.k ? (a.hkv + 3) / 4 : 0);
+  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t step = (int64_t)gridDim.x * kWarps / SPLIT;
+  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
+  const int row = lane >> 3;  // of an item's four heads
+  const int o1 = row * kHeadDim + 8 * p.c1, o2 = row * kHeadDim + 8 * p.c2;
+  pdl_wait();
+  pdl_trigger();
 
-  for (int i = threadIdx.x; i < ntok * (a.rope.dim / 2); i += kThreads) {
-    const int t = i / (a.rope.dim / 2), f = i % (a.rope.dim / 2);
-    const int64_t pos = a.pos[tok0 + t];
-    if (!bad_rope_position(pos)) rope_angle(a.rope, pos, f, s_cos[t], s_sin[t]);
-  }
+  Walk at{gw / SPLIT, sub0};
+  Walk far = at;  // the next item to load
+  const int64_t end = sub0 < per ? a.n : 0;
+  int in = 0;  // its place in the ring
+  auto load = [&]() {
+    if (far.tok < end) {
+      const bool is_k = far.sub >= nq;
+      const int it = is_k ? far.sub - nq : far.sub;
+      const bool there = 4 * it + row < (is_k ? a.hkv : a.hq);
+      const __nv_bfloat16* src = (is_k ? a.k + far.tok * a.k_stride : a.q + far.tok * a.q_stride) +
+                                 it * 4 * kHeadDim;
+      copy16_if(smem_u32(&s_ring[warp][in][0][lane]), src + (there ? o1 : 0), there);
+      copy16_if(smem_u32(&s_ring[warp][in][1][lane]), src + (there ? o2 : 0), there);
+      next_item<SPLIT>(far, sub0, per, step);
+      in = in == kAhead ? 0 : in + 1;
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) load();
   load_norm_weights(a.norm, s_w);
-  if (threadIdx.x < ntok && a.status) {
-    const int64_t pos = a.pos[tok0 + threadIdx.x];
-    if (bad_rope_position(pos)) atomicOr(a.status, rope_position_flag(pos));
-  }
   __syncthreads();
 
-  for (int it = warp; it < ntok * per; it += kWarps) {
-    const int t = it / per, sub = it % per;
-    const int64_t tok = tok0 + t;
-    const bool is_k = sub >= nq;
-    const int head = 4 * (is_k ? sub - nq : sub) + (lane >> 3);
+  RowCoef coef;
+  int64_t tok = -1;
+  int side = -1;  // whose coefficients (0: q, 1: k), of token tok
+  bool bad = false;
+  int64_t next_pos = at.tok < end ? a.pos[at.tok] : 0;
+  for (int out = 0; at.tok < end; next_item<SPLIT>(at, sub0, per, step)) {
+    const bool is_k = at.sub >= nq;
+    const bool norm = (is_k ? a.norm.wk : a.norm.wq) != nullptr;
+    if (at.tok != tok) {
+      const int64_t pos = next_pos;
+      if (at.tok + step < end) next_pos = a.pos[at.tok + step];
+      bad = bad_rope_position(pos);
+      if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
+      rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+      side = -1;
+      tok = at.tok;
+    }
+    if (is_k != side) {
+      side = is_k;
+      row_coef<INTER>(p, norm, s_w + (is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+    }
+    load();
+    copies_wait<kAhead>();
+    float u[8], v[8];
+    unpack_pairs<INTER>(s_ring[warp][out][0][lane], s_ring[warp][out][1][lane], u, v);
+    out = out == kAhead ? 0 : out + 1;
+    norm_and_turn(p, norm, coef, a.norm.eps, u, v);
+    uint4 y1, y2;
+    pack_pairs<INTER>(u, v, y1, y2);
+    if (bad) y1 = y2 = make_uint4(0, 0, 0, 0);
+    const int it = is_k ? at.sub - nq : at.sub;
     const int heads = is_k ? a.hkv : a.hq;
-    const bool live = head < heads;
-    const __nv_bfloat16* src =
-        (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + head * kHeadDim;
-    __nv_bfloat16* dst = (is_k ? a.k_out : a.q_out) + (tok * heads + head) * kHeadDim;
-    uint4 v1 = make_uint4(0, 0, 0, 0), v2 = v1;
-    if (live) {
-      v1 = *reinterpret_cast<const uint4*>(src + 8 * p.c1);
-      v2 = *reinterpret_cast<const uint4*>(src + 8 * p.c2);
-    }
-    float x[16];
-    unpack8(v1, x);
-    unpack8(v2, x + 8);
-    norm_and_turn(a.rope, p, (is_k ? a.norm.wk : a.norm.wq) != nullptr,
-                  s_w + (is_k ? kHeadDim : 0), a.norm.eps, s_cos[t], s_sin[t], x);
-    if (bad_rope_position(a.pos[tok])) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    }
-    if (live) {
-      *reinterpret_cast<uint4*>(dst + 8 * p.c1) = pack8(x);
-      *reinterpret_cast<uint4*>(dst + 8 * p.c2) = pack8(x + 8);
+    if (4 * it + row < heads) {
+      __nv_bfloat16* dst =
+          (is_k ? a.k_out : a.q_out) + at.tok * heads * kHeadDim + it * 4 * kHeadDim;
+      *reinterpret_cast<uint4*>(dst + o1) = y1;
+      *reinterpret_cast<uint4*>(dst + o2) = y2;
     }
   }
 }
 
-// Backward; blocks stride over groups of kBwdTokens tokens and keep their share of the weights'
-// gradients in registers: every lane holds sixteen dims of q's and of k's.
-constexpr int kBwdTokens = 4;
-
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeBwdArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ __align__(16) float s_cos[kBwdTokens][kHalfDim];
-  __shared__ __align__(16) float s_sin[kBwdTokens][kHalfDim];
+// Backward.  A warp keeps its share of the query weight's gradient in registers, of the key
+// weight's in shared memory (a token has fewer key heads).
+template <int SPLIT, bool INTER>
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
+    norm_rope_bwd_kernel(const NormRopeBwdArgs a) {
+  extern __shared__ __align__(16) uint4 s_ring[];  // [kWarps][kBwdAhead + 1][4][32]
+  __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
+  __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
+  __shared__ uint64_t s_dwk[kWarps][8][32];  // a lane's sixteen sums, in pairs
   __shared__ float s_dw[kWarps][2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RopeLane p = rope_lane(a.rope, lane & 7);
+  const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
   const int nq = a.dq_out ? (a.hq + 3) / 4 : 0;
-  const int nk = a.dk_out ? (a.hkv + 3) / 4 : 0;
-  const int per = nq + nk;
-  float dwq[16], dwk[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) dwq[i] = dwk[i] = 0.f;
-  load_norm_weights(a.norm, s_w);
+  const int per = nq + (a.dk_out ? (a.hkv + 3) / 4 : 0);
+  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t step = (int64_t)gridDim.x * kWarps / SPLIT;
+  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
+  const int row = lane >> 3;
+  const int o1 = row * kHeadDim + 8 * p.c1, o2 = row * kHeadDim + 8 * p.c2;
+  const bool norm_q = a.norm.wq != nullptr, norm_k = a.norm.wk != nullptr;
+  uint4* ring = s_ring + warp * (kBwdAhead + 1) * 4 * 32 + lane;
+  pdl_wait();
+  pdl_trigger();
 
-  for (int64_t tok0 = (int64_t)blockIdx.x * kBwdTokens; tok0 < a.n;
-       tok0 += (int64_t)gridDim.x * kBwdTokens) {
-    const int ntok = static_cast<int>(a.n - tok0 < kBwdTokens ? a.n - tok0 : kBwdTokens);
-    __syncthreads();
-    for (int i = threadIdx.x; i < ntok * (a.rope.dim / 2); i += kThreads) {
-      const int t = i / (a.rope.dim / 2), f = i % (a.rope.dim / 2);
-      const int64_t pos = a.pos[tok0 + t];
-      if (!bad_rope_position(pos)) rope_angle(a.rope, pos, f, s_cos[t], s_sin[t]);
-    }
-    if (threadIdx.x < ntok && a.status) {
-      const int64_t pos = a.pos[tok0 + threadIdx.x];
-      if (bad_rope_position(pos)) atomicOr(a.status, rope_position_flag(pos));
-    }
-    __syncthreads();
-    for (int it = warp; it < ntok * per; it += kWarps) {
-      const int t = it / per, sub = it % per;
-      const int64_t tok = tok0 + t;
-      const bool is_k = sub >= nq;
-      const int head = 4 * (is_k ? sub - nq : sub) + (lane >> 3);
+  Walk at{gw / SPLIT, sub0};
+  Walk far = at;
+  const int64_t end = sub0 < per ? a.n : 0;
+  int in = 0;
+  auto load = [&]() {
+    if (far.tok < end) {
+      const bool is_k = far.sub >= nq;
+      const int it = is_k ? far.sub - nq : far.sub;
       const int heads = is_k ? a.hkv : a.hq;
-      const bool bad = bad_rope_position(a.pos[tok]);
-      const bool live = head < heads;
-      const bool norm = (is_k ? a.norm.wk : a.norm.wq) != nullptr;
-      const __nv_bfloat16* gsrc =
-          (is_k ? a.dk_out : a.dq_out) + (tok * heads + head) * kHeadDim;
-      const __nv_bfloat16* xsrc =
-          (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + head * kHeadDim;
-      __nv_bfloat16* dst =
-          (is_k ? a.dk + tok * a.dk_stride : a.dq + tok * a.dq_stride) + head * kHeadDim;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      uint4 g1 = z, g2 = z, x1 = z, x2 = z;
-      if (live && !bad) {
-        g1 = *reinterpret_cast<const uint4*>(gsrc + 8 * p.c1);
-        g2 = *reinterpret_cast<const uint4*>(gsrc + 8 * p.c2);
-        if (norm) {
-          x1 = *reinterpret_cast<const uint4*>(xsrc + 8 * p.c1);
-          x2 = *reinterpret_cast<const uint4*>(xsrc + 8 * p.c2);
-        }
+      const bool there = 4 * it + row < heads;
+      const __nv_bfloat16* g =
+          (is_k ? a.dk_out : a.dq_out) + far.tok * heads * kHeadDim + it * 4 * kHeadDim;
+      uint4* dst = ring + in * 4 * 32;
+      copy16_if(smem_u32(dst), g + (there ? o1 : 0), there);
+      copy16_if(smem_u32(dst + 32), g + (there ? o2 : 0), there);
+      if (is_k ? norm_k : norm_q) {
+        const __nv_bfloat16* x =
+            (is_k ? a.k + far.tok * a.k_stride : a.q + far.tok * a.q_stride) + it * 4 * kHeadDim;
+        copy16_if(smem_u32(dst + 64), x + (there ? o1 : 0), there);
+        copy16_if(smem_u32(dst + 96), x + (there ? o2 : 0), there);
       }
-      float g[16];
-      unpack8(g1, g);
-      unpack8(g2, g + 8);
-      if (!bad) rope_turn<-1>(a.rope, p, s_cos[t], s_sin[t], g);
+      next_item<SPLIT>(far, sub0, per, step);
+      in = in == kBwdAhead ? 0 : in + 1;
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kBwdAhead; ++i) load();
+  load_norm_weights(a.norm, s_w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_dwk[warp][i][lane] = 0;
+  __syncthreads();
+
+  float dwu[8], dwv[8];  // query weight's gradient, this lane's pairs
+  float wu[8], wv[8], c[8], s[8], ns[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dwu[i] = dwv[i] = 0.f;
+  int64_t tok = -1;
+  int side = -1;  // whose weights are in wu, wv
+  bool bad = false;
+  int64_t next_pos = at.tok < end ? a.pos[at.tok] : 0;
+  for (int out = 0; at.tok < end; next_item<SPLIT>(at, sub0, per, step)) {
+    const bool is_k = at.sub >= nq;
+    const bool norm = is_k ? norm_k : norm_q;
+    if (at.tok != tok) {
+      const int64_t pos = next_pos;
+      if (at.tok + step < end) next_pos = a.pos[at.tok + step];
+      bad = bad_rope_position(pos);
+      if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
+      rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+      lane_angles(p, s_cos[warp], s_sin[warp], c, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ns[i] = -s[i];
+      tok = at.tok;
+    }
+    if (is_k != side) {
+      side = is_k;
+      lane_weights<INTER>(s_w + (is_k ? kHeadDim : 0), p, wu, wv);
+    }
+    load();
+    copies_wait<kBwdAhead>();
+    const uint4* r = ring + out * 4 * 32;
+    out = out == kBwdAhead ? 0 : out + 1;
+    const int it = is_k ? at.sub - nq : at.sub;
+    const int heads = is_k ? a.hkv : a.hq;
+    const bool live = 4 * it + row < heads;
+    uint4 y1 = make_uint4(0, 0, 0, 0), y2 = y1;
+    if (!bad) {
+      float gu[8], gv[8];
+      unpack_pairs<INTER>(r[0], r[32], gu, gv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < 2 ? p.rot1 : p.rot2) {
+          const uint64_t x = pair_of(gu, i), y = pair_of(gv, i);
+          set_pair(gu, i, ffma2(y, pair_of(s, i), fmul2(x, pair_of(c, i))));
+          set_pair(gv, i, ffma2(x, pair_of(ns, i), fmul2(y, pair_of(c, i))));
+        }
       if (norm) {
-        float x[16], w[16];
-        unpack8(x1, x);
-        unpack8(x2, x + 8);
-        const float rstd = row_rstd(x, a.norm.eps);
-        lane_weights(s_w + (is_k ? kHeadDim : 0), p, w);
-        float dot = 0.f;
+        float nu[8], nv[8];
+        unpack_pairs<INTER>(r[64], r[96], nu, nv);
+        float rstd = row_rstd(nu, nv, a.norm.eps);
+        if (!live) rstd = 0.f;  // (eps may be 0)
+        const uint64_t r2 = pack_f32x2(rstd, rstd);
+        uint64_t dot = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] *= rstd;  // n
-          const float gn = (live && !bad) ? g[i] * x[i] : 0.f;
-          if (is_k) dwk[i] += gn; else dwq[i] += gn;
-          dot = fmaf(w[i], gn, dot);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t x = fmul2(pair_of(nu, i), r2), y = fmul2(pair_of(nv, i), r2);
+          const uint64_t gx = pair_of(gu, i), gy = pair_of(gv, i);
+          set_pair(nu, i, x);
+          set_pair(nv, i, y);
+          if (is_k) {
+            s_dwk[warp][i][lane] = ffma2(gx, x, s_dwk[warp][i][lane]);
+            s_dwk[warp][4 + i][lane] = ffma2(gy, y, s_dwk[warp][4 + i][lane]);
+          } else {
+            set_pair(dwu, i, ffma2(gx, x, pair_of(dwu, i)));
+            set_pair(dwv, i, ffma2(gy, y, pair_of(dwv, i)));
+          }
+          const uint64_t hx = fmul2(gx, pair_of(wu, i)), hy = fmul2(gy, pair_of(wv, i));
+          dot = ffma2(hy, y, ffma2(hx, x, dot));
+          set_pair(gu, i, hx);
+          set_pair(gv, i, hy);
         }
-        const float mean = row_sum(dot) * (1.f / kHeadDim);
+        const float2 d = unpack_f32x2(dot);
+        const float mean = row_sum(d.x + d.y) * (-1.f / kHeadDim);
+        const uint64_t m2 = pack_f32x2(mean, mean);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = rstd * (w[i] * g[i] - x[i] * mean);
+        for (int i = 0; i < 4; ++i) {
+          set_pair(gu, i, fmul2(r2, ffma2(pair_of(nu, i), m2, pair_of(gu, i))));
+          set_pair(gv, i, fmul2(r2, ffma2(pair_of(nv, i), m2, pair_of(gv, i))));
+        }
       }
-      if (live) {
-        uint4 y1 = pack8(g), y2 = pack8(g + 8);
-        if (bad) y1 = y2 = z;
-        *reinterpret_cast<uint4*>(dst + 8 * p.c1) = y1;
-        *reinterpret_cast<uint4*>(dst + 8 * p.c2) = y2;
-      }
+      pack_pairs<INTER>(gu, gv, y1, y2);
+    }
+    if (live) {
+      __nv_bfloat16* dst = (is_k ? a.dk + at.tok * a.dk_stride : a.dq + at.tok * a.dq_stride) +
+                           it * 4 * kHeadDim;
+      *reinterpret_cast<uint4*>(dst + o1) = y1;
+      *reinterpret_cast<uint4*>(dst + o2) = y2;
     }
   }
   if (!a.partial) return;
   // the four rows of a warp, then the eight warps in order: one partial row a block
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], 8);
-    dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], 16);
-    dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], 8);
-    dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], 16);
-  }
-  if (lane < 8) {
+  for (int i = 0; i < 8; ++i) {
+    const float2 ku = unpack_f32x2(s_dwk[warp][i >> 1][lane]);
+    const float2 kv = unpack_f32x2(s_dwk[warp][4 + (i >> 1)][lane]);
+    float x[4] = {dwu[i], dwv[i], (i & 1) ? ku.y : ku.x, (i & 1) ? kv.y : kv.x};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int d = 8 * (i < 8 ? p.c1 : p.c2) + (i & 7);
-      s_dw[warp][d] = dwq[i];
-      s_dw[warp][kHeadDim + d] = dwk[i];
+    for (int j = 0; j < 4; ++j) {
+      x[j] += __shfl_xor_sync(0xffffffffu, x[j], 8);
+      x[j] += __shfl_xor_sync(0xffffffffu, x[j], 16);
+    }
+    if (lane < 8) {
+      const int du = INTER ? 8 * (i < 4 ? p.c1 : p.c2) + 2 * (i & 3) : 8 * p.c1 + i;
+      const int dv = INTER ? du + 1 : 8 * p.c2 + i;
+      s_dw[warp][du] = x[0];
+      s_dw[warp][dv] = x[1];
+      s_dw[warp][kHeadDim + du] = x[2];
+      s_dw[warp][kHeadDim + dv] = x[3];
     }
   }
   __syncthreads();
-  float s = 0.f;
+  float sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += s_dw[w][threadIdx.x];
-  a.partial[(int64_t)blockIdx.x * (2 * kHeadDim) + threadIdx.x] = s;
+  for (int w = 0; w < kWarps; ++w) sum += s_dw[w][threadIdx.x];
+  a.partial[(int64_t)blockIdx.x * (2 * kHeadDim) + threadIdx.x] = sum;
 }
 
 // dw[d] = the blocks' partials added up in block order: 32 columns a block, eight threads a
@@ -204,6 +286,7 @@ __global__ void __launch_bounds__(256)
   __shared__ float s[8][32];
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
   float v = 0.f;
+#pragma unroll 8
   for (int r = part; r < rows; r += 8) v += partial[(int64_t)r * (2 * kHeadDim) + col];
   s[part][threadIdx.x & 31] = v;
   __syncthreads();
@@ -216,33 +299,60 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-int64_t bwd_grid(int64_t n) {
-  const int64_t groups = (n + kBwdTokens - 1) / kBwdTokens;
-  const int64_t most = 2 * (int64_t)sm_count();
-  return groups < most ? groups : most;
+// Tokens below which eight warps share one: fewer than one a warp slot of the whole GPU.
+bool split_tokens(int64_t n) { return n < 16 * (int64_t)sm_count(); }
+
+// One wave of blocks, or as many as there are tokens for.
+int64_t wave_grid(int64_t n, int per_sm) {
+  const int64_t blocks = split_tokens(n) ? n : (n + kWarps - 1) / kWarps;
+  const int64_t most = per_sm * (int64_t)sm_count();
+  return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
 }  // namespace
 
 size_t norm_rope_bwd_workspace_bytes(int64_t n) {
-  return size_t(bwd_grid(n > 0 ? n : 1)) * 2 * kHeadDim * sizeof(float);
+  return size_t(wave_grid(n, kBwdBlocksPerSm)) * 2 * kHeadDim * sizeof(float);
+}
+
+template <int SPLIT, bool INTER>
+static int launch_forward(const NormRopeArgs& a, cudaStream_t stream) {
+  constexpr size_t ring = kWarps * (kAhead + 1) * 2 * 32 * sizeof(uint4);
+  PS_TRY((allow_smem<norm_rope_kernel<SPLIT, INTER>>(ring)));
+  return check_cuda(
+      launch_pdl(norm_rope_kernel<SPLIT, INTER>,
+                 dim3(static_cast<unsigned>(wave_grid(a.n, kBlocksPerSm))), dim3(kThreads), ring,
+                 stream, a),
+      "norm_rope_kernel launch");
 }
 
 int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  // four tokens a block share the set-up once there are blocks enough for every SM
-  const bool wide = a.n > 8 * (int64_t)sm_count();
-  const int64_t grid = wide ? (a.n + 3) / 4 : a.n;
-  if (grid > 0x7fffffff) return fail(PS_ERR_UNSUPPORTED, "too many tokens");
-  return check_cuda(launch_pdl(wide ? norm_rope_kernel<4> : norm_rope_kernel<1>,
-                               dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a),
-                    "norm_rope_kernel launch");
+  if (split_tokens(a.n))
+    return a.rope.interleaved ? launch_forward<kWarps, true>(a, stream)
+                              : launch_forward<kWarps, false>(a, stream);
+  return a.rope.interleaved ? launch_forward<1, true>(a, stream)
+                            : launch_forward<1, false>(a, stream);
+}
+
+template <int SPLIT, bool INTER>
+static int launch_backward(const NormRopeBwdArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr size_t ring = kWarps * (kBwdAhead + 1) * 4 * 32 * sizeof(uint4);
+  PS_TRY((allow_smem<norm_rope_bwd_kernel<SPLIT, INTER>>(ring)));
+  return check_cuda(launch_pdl(norm_rope_bwd_kernel<SPLIT, INTER>,
+                               dim3(static_cast<unsigned>(grid)), dim3(kThreads), ring, stream, a),
+                    "norm_rope_bwd_kernel launch");
 }
 
 int launch_norm_rope_bwd(const NormRopeBwdArgs& a, float* dwq, float* dwk, cudaStream_t stream) {
-  const int64_t grid = bwd_grid(a.n > 0 ? a.n : 1);  // no tokens: the weights' gradients are 0
-  PS_TRY(check_cuda(launch_pdl(norm_rope_bwd_kernel, dim3(static_cast<unsigned>(grid)),
-                               dim3(kThreads), 0, stream, a),
-                    "norm_rope_bwd_kernel launch"));
+  const int64_t grid = wave_grid(a.n, kBwdBlocksPerSm);  // (no tokens: one block leaves zeros)
+  int rc;
+  if (split_tokens(a.n))
+    rc = a.rope.interleaved ? launch_backward<kWarps, true>(a, grid, stream)
+                            : launch_backward<kWarps, false>(a, grid, stream);
+  else
+    rc = a.rope.interleaved ? launch_backward<1, true>(a, grid, stream)
+                            : launch_backward<1, false>(a, grid, stream);
+  PS_TRY(rc);
   if (!dwq && !dwk) return PS_OK;
   return check_cuda(launch_pdl(norm_rope_dw_kernel, dim3(2 * kHeadDim / 32), dim3(256), 0, stream,
                                static_cast<const float*>(a.partial), static_cast<int32_t>(grid),

@@ -8,6 +8,11 @@
 //     the unrotated chunks 2m .. 15 go two by two to the other lanes
 //   interleaved: chunks (l, l + 8); pairs (2i, 2i + 1) never leave a chunk
 // A warp takes four heads of one token at a time; q and k heads are never mixed in one item.
+//
+// A lane's eight pairs (u, v) become rstd (u a - v b), rstd (v c + u d) with coefficients that hold
+// the weights and the angles, a = w_u cos, b = w_v sin, c = w_v cos, d = w_u sin: formed once for
+// all heads of a token, they leave six operations a pair (340 -> 150 instructions per four heads
+// with the loads, where HBM allows 350).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,16 +24,19 @@ namespace ps {
 
 constexpr int kHalfDim = kHeadDim / 2;
 
-// Where a lane's two chunks are and which angles turn them.
+// Where a lane's two chunks are and which angles turn them.  Pairs 0..3 and 4..7 of a lane are
+// rotated or not together: in the half layout pair e is (chunk 1, chunk 2) dim e, interleaved pair
+// j is dims 2 j, 2 j + 1 of chunk 1, and pair 4 + j of chunk 2.
 struct RopeLane {
-  int c1, c2;      // chunks (dims 8 c .. 8 c + 7)
-  int a1, a2;      // first of four angle indices each: half layout (8 l, 8 l + 4)
-  bool rot1, rot2; // whether the chunk is rotated
+  int c1, c2;       // chunks (dims 8 c .. 8 c + 7)
+  int a1, a2;       // angles of pairs 0..3 start at a1, of 4..7 at a2
+  bool rot1, rot2;  // whether pairs 0..3 and 4..7 are rotated
 };
 
+template <bool INTER>
 __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   RopeLane p;
-  if (r.interleaved) {
+  if (INTER) {
     p.c1 = l;
     p.c2 = l + 8;
     p.rot1 = 8 * l < r.dim;
@@ -46,31 +54,70 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   return p;
 }
 
-// Angles of one token, 64-bit range reduction (rope_cos_sin), into cos[i], sin[i].
-__device__ __forceinline__ void rope_angle(const RopeArgs& r, int64_t pos, int i, float* cos,
-                                           float* sin) {
-  const float2 cs = rope_cos_sin(double(pos), r.inv_freq[i]);
-  cos[i] = cs.x * r.attn;
-  sin[i] = cs.y * r.attn;
-}
-
 __device__ __forceinline__ bool bad_rope_position(int64_t p) { return p < 0 || p >= (1ll << 31); }
 __device__ __forceinline__ int32_t rope_position_flag(int64_t p) {
   return p < 0 ? PS_DEV_BAD_POS : PS_DEV_POS_RANGE;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane's chunks as pairs and back; INTER: the interleaved layout (a template parameter: as a
+// flag it costs a select an element).
+template <bool INTER>
+__device__ __forceinline__ void unpack_pairs(const uint4& c1, const uint4& c2, float (&u)[8],
+                                             float (&v)[8]) {
+  const uint32_t a[4] = {c1.x, c1.y, c1.z, c1.w}, b[4] = {c2.x, c2.y, c2.z, c2.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float al = __uint_as_float(a[i] << 16), ah = __uint_as_float(a[i] & 0xffff0000u);
+    const float bl = __uint_as_float(b[i] << 16), bh = __uint_as_float(b[i] & 0xffff0000u);
+    if (INTER) {
+      u[i] = al, v[i] = ah, u[4 + i] = bl, v[4 + i] = bh;
+    } else {
+      u[2 * i] = al, u[2 * i + 1] = ah, v[2 * i] = bl, v[2 * i + 1] = bh;
+    }
+  }
+}
+template <bool INTER>
+__device__ __forceinline__ void pack_pairs(const float (&u)[8], const float (&v)[8], uint4& c1,
+                                           uint4& c2) {
+  if (INTER) {
+    c1 = make_uint4(cvt_bf16x2(u[0], v[0]), cvt_bf16x2(u[1], v[1]), cvt_bf16x2(u[2], v[2]),
+                    cvt_bf16x2(u[3], v[3]));
+    c2 = make_uint4(cvt_bf16x2(u[4], v[4]), cvt_bf16x2(u[5], v[5]), cvt_bf16x2(u[6], v[6]),
+                    cvt_bf16x2(u[7], v[7]));
+  } else {
+    c1 = make_uint4(cvt_bf16x2(u[0], u[1]), cvt_bf16x2(u[2], u[3]), cvt_bf16x2(u[4], u[5]),
+                    cvt_bf16x2(u[6], u[7]));
+    c2 = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                    cvt_bf16x2(v[6], v[7]));
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]), cvt_bf16x2(x[4], x[5]),
-                    cvt_bf16x2(x[6], x[7]));
+// One warp forms all angles of a token, range reduction in 64 bits (rope_cos_sin), into its own
+// cos[64], sin[64] in shared memory.
+__device__ __forceinline__ void rope_angles(const RopeArgs& r, int64_t pos, int lane, float* cos,
+                                            float* sin) {
+  __syncwarp();  // the last token's are no longer read
+  for (int i = lane; i < r.dim / 2; i += 32) {
+    const float2 cs = rope_cos_sin(double(pos), r.inv_freq[i]);
+    cos[i] = cs.x * r.attn;
+    sin[i] = cs.y * r.attn;
+  }
+  __syncwarp();
+}
+
+// The items of a warp, in order: of every `step`-th token four q heads each, then four k heads
+// each, where SPLIT warps share a token every SPLIT-th of them.
+struct Walk {
+  int64_t tok;
+  int32_t sub;  // [0, nq): q item, [nq, nq + nk): k item
+};
+template <int SPLIT>
+__device__ __forceinline__ void next_item(Walk& w, int32_t sub0, int32_t per, int64_t step) {
+  w.sub += SPLIT;
+  if (w.sub >= per) {
+    w.sub = sub0;
+    w.tok += step;
+  }
 }
 
 // Sum over the eight lanes of a row (every lane gets it; the same order in all of them).
@@ -81,52 +128,27 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// 1 / sqrt(mean(x^2) + eps) of a row held by eight lanes, fp32.
-__device__ __forceinline__ float row_rstd(const float (&x)[16], float eps) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s = fmaf(x[i], x[i], s);
-  return rsqrtf(row_sum(s) * (1.f / kHeadDim) + eps);
+// Two neighbouring floats as one operand of the packed fp32 instructions, which do two lanes of
+// the work in one issue.
+__device__ __forceinline__ uint64_t pair_of(const float (&x)[8], int i) {
+  return pack_f32x2(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void set_pair(float (&x)[8], int i, uint64_t v) {
+  const float2 f = unpack_f32x2(v);
+  x[2 * i] = f.x;
+  x[2 * i + 1] = f.y;
 }
 
-// Turns a lane's sixteen values (chunk 1, chunk 2) by the token's angles; DIR -1 turns back.
-template <int DIR>
-__device__ __forceinline__ void rope_turn(const RopeArgs& r, const RopeLane& p, const float* cos,
-                                          const float* sin, float (&x)[16]) {
-  if (!p.rot1) return;  // chunk 2 is rotated only where chunk 1 is
-  const float4 ca = *reinterpret_cast<const float4*>(cos + p.a1);
-  const float4 sa = *reinterpret_cast<const float4*>(sin + p.a1);
-  const float cA[4] = {ca.x, ca.y, ca.z, ca.w};
-  const float sA[4] = {DIR * sa.x, DIR * sa.y, DIR * sa.z, DIR * sa.w};
-  if (r.interleaved) {
+// 1 / sqrt(mean(x^2) + eps) of a row held by eight lanes, fp32.
+__device__ __forceinline__ float row_rstd(const float (&u)[8], const float (&v)[8], float eps) {
+  uint64_t s = 0, t = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = x[2 * j], v = x[2 * j + 1];
-      x[2 * j] = rope_lo(u, v, cA[j], sA[j]);
-      x[2 * j + 1] = rope_hi(u, v, cA[j], sA[j]);
-    }
-    if (!p.rot2) return;
+  for (int i = 0; i < 4; ++i) {
+    s = ffma2(pair_of(u, i), pair_of(u, i), s);
+    t = ffma2(pair_of(v, i), pair_of(v, i), t);
   }
-  const float4 cb = *reinterpret_cast<const float4*>(cos + p.a2);
-  const float4 sb = *reinterpret_cast<const float4*>(sin + p.a2);
-  const float cB[4] = {cb.x, cb.y, cb.z, cb.w};
-  const float sB[4] = {DIR * sb.x, DIR * sb.y, DIR * sb.z, DIR * sb.w};
-  if (r.interleaved) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = x[8 + 2 * j], v = x[9 + 2 * j];
-      x[8 + 2 * j] = rope_lo(u, v, cB[j], sB[j]);
-      x[9 + 2 * j] = rope_hi(u, v, cB[j], sB[j]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = e < 4 ? cA[e & 3] : cB[e & 3], s = e < 4 ? sA[e & 3] : sB[e & 3];
-      const float u = x[e], v = x[8 + e];
-      x[e] = rope_lo(u, v, c, s);
-      x[8 + e] = rope_hi(u, v, c, s);
-    }
-  }
+  const float2 x = unpack_f32x2(fadd2(s, t));
+  return rsqrtf(row_sum(x.x + x.y) * (1.f / kHeadDim) + eps);
 }
 
 // The norm's weights as fp32 in shared memory: [0, 128) queries, [128, 256) keys (1 where there
@@ -141,28 +163,92 @@ __device__ __forceinline__ void load_norm_weights(const NormArgs& n, float* s_w)
   }
 }
 
-__device__ __forceinline__ void lane_weights(const float* w, const RopeLane& p, float (&out)[16]) {
+// A lane's weights as pairs.
+template <bool INTER>
+__device__ __forceinline__ void lane_weights(const float* w, const RopeLane& p, float (&wu)[8],
+                                             float (&wv)[8]) {
+  float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const float4 a = *reinterpret_cast<const float4*>(w + 8 * p.c1 + 4 * i);
     const float4 b = *reinterpret_cast<const float4*>(w + 8 * p.c2 + 4 * i);
-    out[4 * i] = a.x, out[4 * i + 1] = a.y, out[4 * i + 2] = a.z, out[4 * i + 3] = a.w;
-    out[8 + 4 * i] = b.x, out[9 + 4 * i] = b.y, out[10 + 4 * i] = b.z, out[11 + 4 * i] = b.w;
+    x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = a.z, x[4 * i + 3] = a.w;
+    y[4 * i] = b.x, y[4 * i + 1] = b.y, y[4 * i + 2] = b.z, y[4 * i + 3] = b.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (INTER) {
+      wu[i] = x[2 * i], wv[i] = x[2 * i + 1], wu[4 + i] = y[2 * i], wv[4 + i] = y[2 * i + 1];
+    } else {
+      wu[2 * i] = x[2 * i], wu[2 * i + 1] = x[2 * i + 1];
+      wv[2 * i] = y[2 * i], wv[2 * i + 1] = y[2 * i + 1];
+    }
   }
 }
 
-// Norm (where `norm`) and rotation of a lane's sixteen raw values, in fp32.
-__device__ __forceinline__ void norm_and_turn(const RopeArgs& r, const RopeLane& p, bool norm,
-                                              const float* s_w, float eps, const float* cos,
-                                              const float* sin, float (&x)[16]) {
-  if (norm) {
-    float w[16];
-    const float rstd = row_rstd(x, eps);
-    lane_weights(s_w, p, w);
+// A lane's cosines and sines (1 and 0 where a pair is not rotated).
+__device__ __forceinline__ void lane_angles(const RopeLane& p, const float* cos, const float* sin,
+                                            float (&c)[8], float (&s)[8]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = x[i] * rstd * w[i];
+  for (int i = 0; i < 2; ++i) {
+    const bool rot = i ? p.rot2 : p.rot1;
+    float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rot) {
+      x = *reinterpret_cast<const float4*>(cos + (i ? p.a2 : p.a1));
+      y = *reinterpret_cast<const float4*>(sin + (i ? p.a2 : p.a1));
+    }
+    c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+    s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
   }
-  rope_turn<1>(r, p, cos, sin, x);
+}
+
+// What turns a lane's pairs of one token's q (or k) heads: with a norm the weights are in it, and
+// b is negative.
+struct RowCoef {
+  float a[8], b[8], c[8], d[8];
+};
+template <bool INTER>
+__device__ __forceinline__ void row_coef(const RopeLane& p, bool norm, const float* w,
+                                         const float* cos, const float* sin, RowCoef& k) {
+  float c[8], s[8], wu[8], wv[8];
+  lane_angles(p, cos, sin, c, s);
+  lane_weights<INTER>(w, p, wu, wv);  // (ones where there is no norm)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    k.a[i] = norm ? wu[i] * c[i] : c[i];
+    k.b[i] = norm ? -wv[i] * s[i] : s[i];
+    k.c[i] = norm ? wv[i] * c[i] : c[i];
+    k.d[i] = norm ? wu[i] * s[i] : s[i];
+  }
+}
+
+// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.  Without a norm the products
+// are rounded as everywhere else that the library rotates, so such rows are bit-identical.
+__device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, const RowCoef& k,
+                                              float eps, float (&u)[8], float (&v)[8]) {
+  if (norm) {
+    const float rstd = row_rstd(u, v, eps);
+    const uint64_t r2 = pack_f32x2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t uu = pair_of(u, i), vv = pair_of(v, i);
+      uint64_t x = fmul2(uu, pair_of(k.a, i)), y = fmul2(vv, pair_of(k.c, i));
+      if (i < 2 ? p.rot1 : p.rot2) {  // (an infinity reaches its own pair only)
+        x = ffma2(vv, pair_of(k.b, i), x);
+        y = ffma2(uu, pair_of(k.d, i), y);
+      }
+      set_pair(u, i, fmul2(x, r2));
+      set_pair(v, i, fmul2(y, r2));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < 4 ? p.rot1 : p.rot2) {
+        const float x = rope_lo(u[i], v[i], k.a[i], k.b[i]);
+        v[i] = rope_hi(u[i], v[i], k.c[i], k.d[i]);
+        u[i] = x;
+      }
+  }
 }
 
 }  // namespace ps
