@@ -30,31 +30,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
   __shared__ __align__(16) float s_w[2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
-  const int nq = a.q ? (a.hq + 3) / 4 : 0;
-  const int per = nq + (a.k ? (a.hkv + 3) / 4 : 0);
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t step = (int64_t)gridDim.x * kWarps / SPLIT;
-  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
+  const Items<SPLIT> items((int64_t)gridDim.x * kWarps / SPLIT, static_cast<int>(gw % SPLIT),
+                           a.q ? a.hq : 0, a.k ? a.hkv : 0);
   const int row = lane >> 3;  // of an item's four heads
-  const int o1 = row * kHeadDim + 8 * p.c1, o2 = row * kHeadDim + 8 * p.c2;
+  const int o1 = row * kHeadDim + 8 * p.c1, d2 = 8 * (p.c2 - p.c1);
   pdl_wait();
   pdl_trigger();
 
-  Walk at{gw / SPLIT, sub0};
-  Walk far = at;  // the next item to load
-  const int64_t end = sub0 < per ? a.n : 0;
-  int in = 0;  // its place in the ring
+  const int64_t end = items.any() ? a.n : 0;
+  Segment at = items.first(gw / SPLIT), far = at;  // the item worked on, the next to load
+  auto source = [&](const Segment& g) {
+    return g.is_k ? a.k + g.tok * a.k_stride + items.k0 * 4 * kHeadDim + o1
+                  : a.q + g.tok * a.q_stride + items.q0 * 4 * kHeadDim + o1;
+  };
+  const __nv_bfloat16* src = source(far);
+  const uint32_t ring = smem_u32(&s_ring[warp][0][0][lane]);
+  constexpr uint32_t kItem = 2 * 32 * sizeof(uint4), kRing = (kAhead + 1) * kItem;
+  uint32_t in = 0;  // the next item's place in the ring
   auto load = [&]() {
     if (far.tok < end) {
-      const bool is_k = far.sub >= nq;
-      const int it = is_k ? far.sub - nq : far.sub;
-      const bool there = 4 * it + row < (is_k ? a.hkv : a.hq);
-      const __nv_bfloat16* src = (is_k ? a.k + far.tok * a.k_stride : a.q + far.tok * a.q_stride) +
-                                 it * 4 * kHeadDim;
-      copy16_if(smem_u32(&s_ring[warp][in][0][lane]), src + (there ? o1 : 0), there);
-      copy16_if(smem_u32(&s_ring[warp][in][1][lane]), src + (there ? o2 : 0), there);
-      next_item<SPLIT>(far, sub0, per, step);
-      in = in == kAhead ? 0 : in + 1;
+      const bool there = row < far.rows;
+      copy16_if(ring + in, src, there);
+      copy16_if(ring + in + kItem / 2, src + d2, there);
+      in = in == kRing - kItem ? 0 : in + kItem;
+      src += items.kStride;
+      if (items.next(far)) src = source(far);
     }
     copies_commit();
   };
@@ -64,43 +65,42 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
   __syncthreads();
 
   RowCoef coef;
-  int64_t tok = -1;
-  int side = -1;  // whose coefficients (0: q, 1: k), of token tok
-  bool bad = false;
+  int64_t tok = -1;  // whose angles are in shared memory
+  bool bad = false, fresh = true;  // fresh: the segment's first item
+  __nv_bfloat16* dst = nullptr;
   int64_t next_pos = at.tok < end ? a.pos[at.tok] : 0;
-  for (int out = 0; at.tok < end; next_item<SPLIT>(at, sub0, per, step)) {
-    const bool is_k = at.sub >= nq;
-    const bool norm = (is_k ? a.norm.wk : a.norm.wq) != nullptr;
-    if (at.tok != tok) {
-      const int64_t pos = next_pos;
-      if (at.tok + step < end) next_pos = a.pos[at.tok + step];
-      bad = bad_rope_position(pos);
-      if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
-      rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
-      side = -1;
-      tok = at.tok;
-    }
-    if (is_k != side) {
-      side = is_k;
-      row_coef<INTER>(p, norm, s_w + (is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+  uint32_t out = 0;
+  while (at.tok < end) {
+    const bool norm = (at.is_k ? a.norm.wk : a.norm.wq) != nullptr;
+    if (fresh) {
+      if (at.tok != tok) {
+        tok = at.tok;
+        const int64_t pos = next_pos;
+        if (tok + items.step < end) next_pos = a.pos[tok + items.step];
+        bad = bad_rope_position(pos);
+        if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
+        rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+      }
+      row_coef<INTER>(p, norm, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+      dst = at.is_k ? a.k_out + (tok * a.hkv + items.k0 * 4) * kHeadDim + o1
+                    : a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
     }
     load();
     copies_wait<kAhead>();
     float u[8], v[8];
-    unpack_pairs<INTER>(s_ring[warp][out][0][lane], s_ring[warp][out][1][lane], u, v);
-    out = out == kAhead ? 0 : out + 1;
+    const uint4* r = &s_ring[warp][0][0][lane] + out / sizeof(uint4);
+    unpack_pairs<INTER>(r[0], r[32], u, v);
+    out = out == kRing - kItem ? 0 : out + kItem;
     norm_and_turn(p, norm, coef, a.norm.eps, u, v);
     uint4 y1, y2;
     pack_pairs<INTER>(u, v, y1, y2);
     if (bad) y1 = y2 = make_uint4(0, 0, 0, 0);
-    const int it = is_k ? at.sub - nq : at.sub;
-    const int heads = is_k ? a.hkv : a.hq;
-    if (4 * it + row < heads) {
-      __nv_bfloat16* dst =
-          (is_k ? a.k_out : a.q_out) + at.tok * heads * kHeadDim + it * 4 * kHeadDim;
-      *reinterpret_cast<uint4*>(dst + o1) = y1;
-      *reinterpret_cast<uint4*>(dst + o2) = y2;
+    if (row < at.rows) {
+      *reinterpret_cast<uint4*>(dst) = y1;
+      *reinterpret_cast<uint4*>(dst + d2) = y2;
     }
+    dst += items.kStride;
+    fresh = items.next(at);
   }
 }
 
@@ -117,41 +117,42 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   __shared__ float s_dw[kWarps][2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
-  const int nq = a.dq_out ? (a.hq + 3) / 4 : 0;
-  const int per = nq + (a.dk_out ? (a.hkv + 3) / 4 : 0);
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t step = (int64_t)gridDim.x * kWarps / SPLIT;
-  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
+  const Items<SPLIT> items((int64_t)gridDim.x * kWarps / SPLIT, static_cast<int>(gw % SPLIT),
+                           a.dq_out ? a.hq : 0, a.dk_out ? a.hkv : 0);
   const int row = lane >> 3;
-  const int o1 = row * kHeadDim + 8 * p.c1, o2 = row * kHeadDim + 8 * p.c2;
+  const int o1 = row * kHeadDim + 8 * p.c1, d2 = 8 * (p.c2 - p.c1);
   const bool norm_q = a.norm.wq != nullptr, norm_k = a.norm.wk != nullptr;
-  uint4* ring = s_ring + warp * (kBwdAhead + 1) * 4 * 32 + lane;
   pdl_wait();
   pdl_trigger();
 
-  Walk at{gw / SPLIT, sub0};
-  Walk far = at;
-  const int64_t end = sub0 < per ? a.n : 0;
-  int in = 0;
+  const int64_t end = items.any() ? a.n : 0;
+  Segment at = items.first(gw / SPLIT), far = at;
+  const __nv_bfloat16 *gsrc, *xsrc;  // the next item's output gradients and inputs
+  auto open = [&](const Segment& g) {
+    const int64_t first = (g.is_k ? items.k0 : items.q0) * 4 * kHeadDim + o1;
+    gsrc = (g.is_k ? a.dk_out + g.tok * a.hkv * kHeadDim : a.dq_out + g.tok * a.hq * kHeadDim) +
+           first;
+    xsrc = (g.is_k ? a.k + g.tok * a.k_stride : a.q + g.tok * a.q_stride) + first;
+  };
+  open(far);
+  const uint4* ring_of = s_ring + warp * (kBwdAhead + 1) * 4 * 32 + lane;
+  const uint32_t ring = smem_u32(ring_of);
+  constexpr uint32_t kItem = 4 * 32 * sizeof(uint4), kRing = (kBwdAhead + 1) * kItem;
+  uint32_t in = 0;
   auto load = [&]() {
     if (far.tok < end) {
-      const bool is_k = far.sub >= nq;
-      const int it = is_k ? far.sub - nq : far.sub;
-      const int heads = is_k ? a.hkv : a.hq;
-      const bool there = 4 * it + row < heads;
-      const __nv_bfloat16* g =
-          (is_k ? a.dk_out : a.dq_out) + far.tok * heads * kHeadDim + it * 4 * kHeadDim;
-      uint4* dst = ring + in * 4 * 32;
-      copy16_if(smem_u32(dst), g + (there ? o1 : 0), there);
-      copy16_if(smem_u32(dst + 32), g + (there ? o2 : 0), there);
-      if (is_k ? norm_k : norm_q) {
-        const __nv_bfloat16* x =
-            (is_k ? a.k + far.tok * a.k_stride : a.q + far.tok * a.q_stride) + it * 4 * kHeadDim;
-        copy16_if(smem_u32(dst + 64), x + (there ? o1 : 0), there);
-        copy16_if(smem_u32(dst + 96), x + (there ? o2 : 0), there);
+      const bool there = row < far.rows;
+      copy16_if(ring + in, gsrc, there);
+      copy16_if(ring + in + kItem / 4, gsrc + d2, there);
+      if (far.is_k ? norm_k : norm_q) {
+        copy16_if(ring + in + kItem / 2, xsrc, there);
+        copy16_if(ring + in + kItem / 4 * 3, xsrc + d2, there);
       }
-      next_item<SPLIT>(far, sub0, per, step);
-      in = in == kBwdAhead ? 0 : in + 1;
+      in = in == kRing - kItem ? 0 : in + kItem;
+      gsrc += items.kStride;
+      xsrc += items.kStride;
+      if (items.next(far)) open(far);
     }
     copies_commit();
   };
@@ -167,34 +168,34 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
 #pragma unroll
   for (int i = 0; i < 8; ++i) dwu[i] = dwv[i] = 0.f;
   int64_t tok = -1;
-  int side = -1;  // whose weights are in wu, wv
-  bool bad = false;
+  bool bad = false, fresh = true;
+  __nv_bfloat16* dst = nullptr;
   int64_t next_pos = at.tok < end ? a.pos[at.tok] : 0;
-  for (int out = 0; at.tok < end; next_item<SPLIT>(at, sub0, per, step)) {
-    const bool is_k = at.sub >= nq;
+  uint32_t out = 0;
+  while (at.tok < end) {
+    const bool is_k = at.is_k;
     const bool norm = is_k ? norm_k : norm_q;
-    if (at.tok != tok) {
-      const int64_t pos = next_pos;
-      if (at.tok + step < end) next_pos = a.pos[at.tok + step];
-      bad = bad_rope_position(pos);
-      if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
-      rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
-      lane_angles(p, s_cos[warp], s_sin[warp], c, s);
+    if (fresh) {
+      if (at.tok != tok) {
+        tok = at.tok;
+        const int64_t pos = next_pos;
+        if (tok + items.step < end) next_pos = a.pos[tok + items.step];
+        bad = bad_rope_position(pos);
+        if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
+        rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+        lane_angles(p, s_cos[warp], s_sin[warp], c, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ns[i] = -s[i];
-      tok = at.tok;
-    }
-    if (is_k != side) {
-      side = is_k;
+        for (int i = 0; i < 8; ++i) ns[i] = -s[i];
+      }
       lane_weights<INTER>(s_w + (is_k ? kHeadDim : 0), p, wu, wv);
+      dst = is_k ? a.dk + tok * a.dk_stride + items.k0 * 4 * kHeadDim + o1
+                 : a.dq + tok * a.dq_stride + items.q0 * 4 * kHeadDim + o1;
     }
     load();
     copies_wait<kBwdAhead>();
-    const uint4* r = ring + out * 4 * 32;
-    out = out == kBwdAhead ? 0 : out + 1;
-    const int it = is_k ? at.sub - nq : at.sub;
-    const int heads = is_k ? a.hkv : a.hq;
-    const bool live = 4 * it + row < heads;
+    const uint4* r = ring_of + out / sizeof(uint4);
+    out = out == kRing - kItem ? 0 : out + kItem;
+    const bool live = row < at.rows;
     uint4 y1 = make_uint4(0, 0, 0, 0), y2 = y1;
     if (!bad) {
       float gu[8], gv[8];
@@ -243,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
       pack_pairs<INTER>(gu, gv, y1, y2);
     }
     if (live) {
-      __nv_bfloat16* dst = (is_k ? a.dk + at.tok * a.dk_stride : a.dq + at.tok * a.dq_stride) +
-                           it * 4 * kHeadDim;
-      *reinterpret_cast<uint4*>(dst + o1) = y1;
-      *reinterpret_cast<uint4*>(dst + o2) = y2;
+      *reinterpret_cast<uint4*>(dst) = y1;
+      *reinterpret_cast<uint4*>(dst + d2) = y2;
     }
+    dst += items.kStride;
+    fresh = items.next(at);
   }
   if (!a.partial) return;
   // the four rows of a warp, then the eight warps in order: one partial row a block

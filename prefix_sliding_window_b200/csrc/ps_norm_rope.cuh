@@ -106,19 +106,38 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& r, int64_t pos, int 
 }
 
 // The items of a warp, in order: of every `step`-th token four q heads each, then four k heads
-// each, where SPLIT warps share a token every SPLIT-th of them.
-struct Walk {
+// each; where SPLIT warps share a token, every SPLIT-th of them.  A segment is one side (q or k) of
+// a token: inside it, pointers move by a constant.
+struct Segment {
   int64_t tok;
-  int32_t sub;  // [0, nq): q item, [nq, nq + nk): k item
+  int32_t rows;  // heads from the item's first one on (fewer than four: a partial item)
+  bool is_k;
 };
 template <int SPLIT>
-__device__ __forceinline__ void next_item(Walk& w, int32_t sub0, int32_t per, int64_t step) {
-  w.sub += SPLIT;
-  if (w.sub >= per) {
-    w.sub = sub0;
-    w.tok += step;
+struct Items {
+  int64_t step;
+  int32_t q0, k0;        // the warp's first q and k item
+  int32_t rows_q, rows_k;  // heads from there on; <= 0: the warp has none on that side
+  static constexpr int kStride = SPLIT * 4 * kHeadDim;  // elements from one item to the next
+
+  __device__ __forceinline__ Items(int64_t step_, int sub, int hq, int hkv) : step(step_), q0(sub) {
+    const int nq = (hq + 3) / 4;
+    k0 = SPLIT == 1 ? 0 : (sub + SPLIT - nq % SPLIT) % SPLIT;
+    rows_q = hq - 4 * q0;
+    rows_k = hkv - 4 * k0;
   }
-}
+  __device__ __forceinline__ bool any() const { return rows_q > 0 || rows_k > 0; }
+  __device__ __forceinline__ Segment first(int64_t tok) const {
+    return rows_q > 0 ? Segment{tok, rows_q, false} : Segment{tok, rows_k, true};
+  }
+  // Moves on; true: to another segment.
+  __device__ __forceinline__ bool next(Segment& s) const {
+    s.rows -= 4 * SPLIT;
+    if (s.rows > 0) return false;
+    s = !s.is_k && rows_k > 0 ? Segment{s.tok, rows_k, true} : first(s.tok + step);
+    return true;
+  }
+};
 
 // Sum over the eight lanes of a row (every lane gets it; the same order in all of them).
 __device__ __forceinline__ float row_sum(float v) {
