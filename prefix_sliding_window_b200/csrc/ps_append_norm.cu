@@ -45,6 +45,18 @@ __device__ __forceinline__ float row_max(float v) {
   return max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
 }
 
+// The same of three.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Quantises a row held by eight lanes (chunks p.c1, p.c2 of a lane, bf16) and writes it: payload
 // words at `pay`, (s, m) of both groups at `rec` (8 bytes).  All lanes take part; only `live` ones
 // write.  A code is the rounded quotient (x - m) / s; the product with 1 / s is within 2e-6 of it,
@@ -60,12 +72,9 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
       x[c][2 * i] = __uint_as_float(w[c][i] << 16);
       x[c][2 * i + 1] = __uint_as_float(w[c][i] & 0xffff0000u);
     }
-    lo[c] = hi[c] = x[c][0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      lo[c] = min_nan(lo[c], x[c][e]);
-      hi[c] = max_nan(hi[c], x[c][e]);
-    }
+    const float* v = x[c];
+    lo[c] = min_nan(min3_nan(min3_nan(v[0], v[1], v[2]), v[3], v[4]), min3_nan(v[5], v[6], v[7]));
+    hi[c] = max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), v[3], v[4]), max3_nan(v[5], v[6], v[7]));
   }
   const int g1 = p.c1 >> 3, g2 = p.c2 >> 3;
   float m[2], s[2];
@@ -77,129 +86,193 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
     s[g] = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(most - m[g], 15.f)));
     if (!(s[g] < INFINITY)) m[g] = s[g] = __uint_as_float(0x7fc00000u);
   }
+  const float round = 12582912.f;  // 1.5 2^23: adding and taking it off rounds to nearest even
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int chunk = c ? p.c2 : p.c1;
     const int g = chunk >> 3, b = chunk & 7;
     const float mm = g ? m[1] : m[0], ss = g ? s[1] : s[0];
     const float inv = __fdiv_rn(1.f, ss);
-    float u[8];
-    bool sure = true;
+    float u[8], off = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = (x[c][e] - mm) * inv;
-      u[e] = rintf(t);
-      sure = sure && fabsf(t - u[e]) < 0.499996f;
+      const float t = __fmul_rn(__fsub_rn(x[c][e], mm), inv);
+      u[e] = __fsub_rn(__fadd_rn(t, round), round);
+      off = max_nan(off, fabsf(__fsub_rn(t, u[e])));
     }
-    if (!sure) {
-#pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        const float q = ss > 0.f ? rintf(__fdiv_rn(x[c][e] - mm, ss)) : 0.f;
+    if (!(off < 0.499996f)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i == e) u[i] = q;
+      for (int e = 0; e < 8; ++e) u[e] = 0.f;
+      if (ss > 0.f) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const float q = rintf(__fdiv_rn(x[c][e] - mm, ss));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i == e) u[i] = q;
+        }
       }
     }
-    // halves of the word as sums of codes times 16^i, exact in fp32
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] = fminf(u[e], 15.f);
-    const float lo16 = fmaf(u[6], 4096.f, fmaf(u[4], 256.f, fmaf(u[2], 16.f, u[0])));
-    const float hi16 = fmaf(u[7], 4096.f, fmaf(u[5], 256.f, fmaf(u[3], 16.f, u[1])));
-    const uint32_t word = static_cast<uint32_t>(lo16) | (static_cast<uint32_t>(hi16) << 16);
-    if (live) *reinterpret_cast<uint32_t*>(pay + 4 * (2 * b + g)) = word;
+    // halves of the word as sums of codes times 16^i, exact in fp32; 2^23 puts them into the
+    // low mantissa bits
+    const float lo16 = fmaf(u[6], 4096.f, fmaf(u[4], 256.f, fmaf(u[2], 16.f, u[0] + 8388608.f)));
+    const float hi16 = fmaf(u[7], 4096.f, fmaf(u[5], 256.f, fmaf(u[3], 16.f, u[1] + 8388608.f)));
+    if (live)
+      *reinterpret_cast<uint32_t*>(pay + 4 * (2 * b + g)) =
+          __byte_perm(__float_as_uint(lo16), __float_as_uint(hi16), 0x5410);
   }
   if (live && lane8 == 0)
     *reinterpret_cast<uint2*>(rec) =
         make_uint2(cvt_bf16x2(s[0], m[0]), cvt_bf16x2(s[1], m[1]));
 }
 
-constexpr int kTokens = 2;  // consecutive tokens of a warp, where there are tokens enough
+constexpr int kAhead = 4;  // items in flight a warp
+constexpr int kBlocksPerSm = 2;
 
-// SPLIT warps share a token (1 or 8).
+// Warps stride over the call's tokens; SPLIT of them share one (1 or 8).  A token's items are four
+// q heads each, then four rows each of its keys and values together (a K row and a V row cost
+// little more in one item than apart, and with two KV heads apart would leave half a warp idle).
 template <int SPLIT, bool Q4, bool INTER>
-__global__ void __launch_bounds__(kThreads, Q4 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     append_norm_kernel(const AppendNormArgs a) {
+  extern __shared__ __align__(16) uint4 s_ring[];  // [kWarps][kAhead + 1][2][32]
   __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
   __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
-  const int nq = a.q ? (a.hq + 3) / 4 : 0;
-  const int nk = (a.hkv + 3) / 4;
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
-  const int sub0 = SPLIT == 1 ? 0 : static_cast<int>(gw % SPLIT);
-  int64_t tok = SPLIT == 1 ? gw * kTokens : gw / SPLIT;
-  int64_t end = tok + (SPLIT == 1 ? kTokens : 1);
-  if (end > a.batch * a.T) end = a.batch * a.T;
+  const Items<SPLIT> items((int64_t)gridDim.x * kWarps / SPLIT, static_cast<int>(gw % SPLIT),
+                           a.q ? a.hq : 0, 2 * a.hkv);
+  const int row = lane >> 3;  // of an item's four rows
+  const int o1 = row * kHeadDim + 8 * p.c1, d2 = 8 * (p.c2 - p.c1);
   pdl_wait();
   pdl_trigger();
+
+  const int64_t end = items.any() ? a.batch * a.T : 0;
+  // where a token's rows go; flag set or stale: nowhere (stale: a newer token of the call owns the
+  // ring slot)
+  struct Token {
+    int64_t pos;
+    StoreRow row;
+    bool stale;
+  };
+  auto token = [&](int64_t tok) {
+    const int64_t b = tok < (int64_t(1) << 32) ? uint32_t(tok) / uint32_t(a.T) : tok / a.T;
+    const int64_t p0 = a.pos0[b];
+    Token t;
+    t.pos = p0 + (tok - b * a.T);
+    t.row = store_row(a.store, a.hkv, b, t.pos);
+    t.stale = !a.store.linear && t.pos >= a.store.lp && t.pos <= p0 + a.T - 1 - a.store.w;
+    return t;
+  };
+  // past the K and V segments of tokens that write none
+  auto settle = [&](Segment& g, bool flag) {
+    while (g.tok < end && g.is_k) {
+      const Token t = token(g.tok);
+      if (flag && t.row.flag && a.status && lane == 0) atomicOr(a.status, t.row.flag);
+      if (!t.row.flag && !t.stale) break;
+      g = items.first(g.tok + items.step);
+    }
+  };
+  Segment at = items.first(gw / SPLIT), far = at;
+  settle(far, false);
+  const __nv_bfloat16* src = nullptr;  // the next q item's
+  auto open = [&]() {
+    if (!far.is_k) src = a.q + far.tok * a.q_stride + items.q0 * 4 * kHeadDim + o1;
+  };
+  open();
+  const uint4* ring_of = s_ring + warp * (kAhead + 1) * 2 * 32 + lane;
+  const uint32_t ring = smem_u32(ring_of);
+  constexpr uint32_t kItem = 2 * 32 * sizeof(uint4), kRing = (kAhead + 1) * kItem;
+  uint32_t in = 0;
+  auto load = [&]() {
+    if (far.tok < end) {
+      const bool there = row < far.rows;
+      const __nv_bfloat16* from = src;
+      if (far.is_k) {
+        const int r = 2 * a.hkv - far.rows + row;
+        from = r < a.hkv ? a.k + far.tok * a.k_stride + r * kHeadDim
+                         : a.v + far.tok * a.v_stride + (r - a.hkv) * kHeadDim;
+        from += 8 * p.c1;
+      }
+      copy16_if(ring + in, from, there);
+      copy16_if(ring + in + kItem / 2, from + d2, there);
+      in = in == kRing - kItem ? 0 : in + kItem;
+      src += items.kStride;
+      if (items.next(far)) {
+        settle(far, false);
+        open();
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) load();
   load_norm_weights(a.norm, s_w);
   __syncthreads();
 
-  for (; tok < end; ++tok) {
-    const int64_t b = tok / a.T;
-    const int64_t p0 = a.pos0[b], pos = p0 + (tok - b * a.T);
-    const StoreRow row = store_row(a.store, a.hkv, b, pos);
-    if (row.flag && sub0 == 0 && a.status && lane == 0) atomicOr(a.status, row.flag);
-    // a token the store has no place for is skipped; its queries become zeros.  A bad table
-    // entry only loses the row.  A row whose ring slot a newer token of the call owns is not written
-    const bool bad = bad_rope_position(pos);
-    const bool skip = bad || (row.flag && !a.store.table);
-    const bool stale =
-        !a.store.linear && pos >= a.store.lp && pos <= p0 + a.T - 1 - a.store.w;
-    const int per = nq + (row.flag || stale ? 0 : 2 * nk);
-
-    auto load = [&](int sub, uint4& r1, uint4& r2) {
-      r1 = r2 = make_uint4(0, 0, 0, 0);
-      if (sub >= per) return;
-      const bool is_q = sub < nq, is_v = sub >= nq + nk;
-      const int head = 4 * (is_q ? sub : is_v ? sub - nq - nk : sub - nq) + (lane >> 3);
-      if (head >= (is_q ? a.hq : a.hkv)) return;
-      const __nv_bfloat16* src = (is_q ? a.q + tok * a.q_stride
-                                       : is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) +
-                                 head * kHeadDim;
-      r1 = *reinterpret_cast<const uint4*>(src + 8 * p.c1);
-      r2 = *reinterpret_cast<const uint4*>(src + 8 * p.c2);
-    };
-    uint4 n1, n2;
-    load(sub0, n1, n2);
-    if (sub0 < per) rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
-    RowCoef coef;
-    int side = -1;  // whose weights are in coef
-    for (int sub = sub0; sub < per; sub += SPLIT) {
-      uint4 r1 = n1, r2 = n2;
-      load(sub + SPLIT, n1, n2);
-      const bool is_q = sub < nq, is_v = sub >= nq + nk;
-      const int head = 4 * (is_q ? sub : is_v ? sub - nq - nk : sub - nq) + (lane >> 3);
-      const bool live = head < (is_q ? a.hq : a.hkv);
-      if (!is_v) {
-        const bool norm = (is_q ? a.norm.wq : a.norm.wk) != nullptr;
-        if (side != is_q) {
-          side = is_q;
-          row_coef<INTER>(p, norm, s_w + (is_q ? 0 : kHeadDim), s_cos[warp], s_sin[warp], coef);
-        }
-        float u[8], v[8];
-        unpack_pairs<INTER>(r1, r2, u, v);
-        norm_and_turn(p, norm, coef, a.norm.eps, u, v);
-        pack_pairs<INTER>(u, v, r1, r2);
-        if (is_q && skip) r1 = r2 = make_uint4(0, 0, 0, 0);
+  RowCoef coef;
+  int64_t tok = -1;  // whose angles are in shared memory
+  bool fresh = true, skip = false;
+  StoreRow place{0, 0, 0, 0};
+  __nv_bfloat16* dst = nullptr;
+  uint32_t out = 0;
+  settle(at, true);
+  while (at.tok < end) {
+    const bool kv = at.is_k;
+    const bool norm = (kv ? a.norm.wk : a.norm.wq) != nullptr;
+    if (fresh) {
+      if (at.tok != tok) {
+        tok = at.tok;
+        const Token t = token(tok);
+        if (t.row.flag && a.status && lane == 0) atomicOr(a.status, t.row.flag);
+        // a token the store has no place for is skipped, its queries become zeros; a bad table
+        // entry only loses the row
+        const bool bad = bad_rope_position(t.pos);
+        skip = bad || (t.row.flag && !a.store.table);
+        place = t.row;
+        rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
       }
-      const int64_t at = row.unit + head * row.stride;
-      if (Q4 && !is_q) {
-        uint8_t* pay = (is_v ? a.store.v[row.ring] : a.store.k[row.ring]) + at * kQ4RowBytes;
-        uint8_t* rec = a.store.s[row.ring] + at * kQ4RecordBytes + (is_v ? 8 : 0);
-        quantise_row(p, r1, r2, live, lane & 7, pay, rec);
-        continue;
-      }
-      __nv_bfloat16* dst =
-          is_q ? a.q_out + (tok * a.hq + head) * kHeadDim
-               : reinterpret_cast<__nv_bfloat16*>(is_v ? a.store.v[row.ring]
-                                                       : a.store.k[row.ring]) + at * kHeadDim;
+      row_coef<INTER>(p, s_w + (kv ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+      if (!kv) dst = a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
+    }
+    load();
+    copies_wait<kAhead>();
+    const uint4 r1 = ring_of[out / sizeof(uint4)], r2 = ring_of[out / sizeof(uint4) + 32];
+    out = out == kRing - kItem ? 0 : out + kItem;
+    float u[8], v[8];
+    unpack_pairs<INTER>(r1, r2, u, v);
+    norm_and_turn(p, norm, coef, a.norm.eps, u, v);
+    uint4 y1, y2;
+    pack_pairs<INTER>(u, v, y1, y2);
+    const bool live = row < at.rows;
+    if (!kv) {
+      if (skip) y1 = y2 = make_uint4(0, 0, 0, 0);
       if (live) {
-        *reinterpret_cast<uint4*>(dst + 8 * p.c1) = r1;
-        *reinterpret_cast<uint4*>(dst + 8 * p.c2) = r2;
+        *reinterpret_cast<uint4*>(dst) = y1;
+        *reinterpret_cast<uint4*>(dst + d2) = y2;
+      }
+      dst += items.kStride;
+    } else {
+      const int r = 2 * a.hkv - at.rows + row;
+      const bool is_v = r >= a.hkv;
+      if (is_v) y1 = r1, y2 = r2;  // values as they are
+      const int64_t to = place.unit + (is_v ? r - a.hkv : r) * place.stride;
+      uint8_t* base = is_v ? a.store.v[place.ring] : a.store.k[place.ring];
+      if (Q4) {
+        quantise_row(p, y1, y2, live, lane & 7, base + to * kQ4RowBytes,
+                     a.store.s[place.ring] + to * kQ4RecordBytes + (is_v ? 8 : 0));
+      } else if (live) {
+        __nv_bfloat16* to_row = reinterpret_cast<__nv_bfloat16*>(base) + to * kHeadDim + 8 * p.c1;
+        *reinterpret_cast<uint4*>(to_row) = y1;
+        *reinterpret_cast<uint4*>(to_row + d2) = y2;
       }
     }
+    fresh = items.next(at);
+    if (fresh) settle(at, true);
   }
 }
 
@@ -248,24 +321,33 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
 
 }  // namespace
 
-template <bool INTER>
-static auto pick_append(bool split, bool q4) {
-  return q4 ? (split ? append_norm_kernel<kWarps, true, INTER> : append_norm_kernel<1, true, INTER>)
-            : (split ? append_norm_kernel<kWarps, false, INTER>
-                     : append_norm_kernel<1, false, INTER>);
+template <int SPLIT, bool Q4, bool INTER>
+static int launch_append(const AppendNormArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr size_t ring = kWarps * (kAhead + 1) * 2 * 32 * sizeof(uint4);
+  PS_TRY((allow_smem<append_norm_kernel<SPLIT, Q4, INTER>>(ring)));
+  return check_cuda(launch_pdl(append_norm_kernel<SPLIT, Q4, INTER>,
+                               dim3(static_cast<unsigned>(grid)), dim3(kThreads), ring, stream, a),
+                    "append_norm_kernel launch");
+}
+
+template <int SPLIT>
+static int launch_append_split(const AppendNormArgs& a, bool q4, int64_t grid,
+                               cudaStream_t stream) {
+  if (q4)
+    return a.rope.interleaved ? launch_append<SPLIT, true, true>(a, grid, stream)
+                              : launch_append<SPLIT, true, false>(a, grid, stream);
+  return a.rope.interleaved ? launch_append<SPLIT, false, true>(a, grid, stream)
+                            : launch_append<SPLIT, false, false>(a, grid, stream);
 }
 
 int launch_append_norm(const AppendNormArgs& a, bool q4, cudaStream_t stream) {
   const int64_t tokens = a.batch * a.T;
   if (tokens <= 0) return PS_OK;
-  const bool split = tokens < 16 * (int64_t)sm_count();  // fewer than one a warp slot
-  const int64_t grid = split ? tokens : (tokens + kWarps * kTokens - 1) / (kWarps * kTokens);
-  if (grid > 0x7fffffff) return fail(PS_ERR_UNSUPPORTED, "too many tokens");
-  auto kern = pick_append<false>(split, q4);
-  if (a.rope.interleaved) kern = pick_append<true>(split, q4);
-  return check_cuda(
-      launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a),
-      "append_norm_kernel launch");
+  // eight warps share a token while every token has a block of its own in one wave
+  const int64_t most = kBlocksPerSm * (int64_t)sm_count();
+  if (tokens <= most) return launch_append_split<kWarps>(a, q4, tokens, stream);
+  const int64_t blocks = (tokens + kWarps - 1) / kWarps;
+  return launch_append_split<1>(a, q4, blocks < most ? blocks : most, stream);
 }
 
 int launch_read_q4(const ReadQ4Args& a, cudaStream_t stream) {

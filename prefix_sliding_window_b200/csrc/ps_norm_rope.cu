@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 3, kAhead = 5;  // items in flight a warp, forward
+constexpr int kBlocksPerSm = 3, kAhead = 4;  // items in flight a warp, forward
 constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 3;  // backward: an item is twice the bytes
 
 // Warps stride over tokens; SPLIT of them share one (1 or 8) and take its items in turn.
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
         if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
         rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
       }
-      row_coef<INTER>(p, norm, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+      row_coef<INTER>(p, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
       dst = at.is_k ? a.k_out + (tok * a.hkv + items.k0 * 4) * kHeadDim + o1
                     : a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
     }
@@ -300,13 +300,14 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Tokens below which eight warps share one: fewer than one a warp slot of the whole GPU.
-bool split_tokens(int64_t n) { return n < 16 * (int64_t)sm_count(); }
+// Eight warps share a token while every token has a block of its own in one wave (1021 tokens, more
+// than that, took 9.5 us shared and XXX one warp each).
+bool split_tokens(int64_t n, int per_sm) { return n <= per_sm * (int64_t)sm_count(); }
 
 // One wave of blocks, or as many as there are tokens for.
 int64_t wave_grid(int64_t n, int per_sm) {
-  const int64_t blocks = split_tokens(n) ? n : (n + kWarps - 1) / kWarps;
   const int64_t most = per_sm * (int64_t)sm_count();
+  const int64_t blocks = split_tokens(n, per_sm) ? n : (n + kWarps - 1) / kWarps;
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
@@ -328,7 +329,7 @@ static int launch_forward(const NormRopeArgs& a, cudaStream_t stream) {
 }
 
 int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream) {
-  if (split_tokens(a.n))
+  if (split_tokens(a.n, kBlocksPerSm))
     return a.rope.interleaved ? launch_forward<kWarps, true>(a, stream)
                               : launch_forward<kWarps, false>(a, stream);
   return a.rope.interleaved ? launch_forward<1, true>(a, stream)
@@ -347,7 +348,7 @@ static int launch_backward(const NormRopeBwdArgs& a, int64_t grid, cudaStream_t 
 int launch_norm_rope_bwd(const NormRopeBwdArgs& a, float* dwq, float* dwk, cudaStream_t stream) {
   const int64_t grid = wave_grid(a.n, kBwdBlocksPerSm);  // (no tokens: one block leaves zeros)
   int rc;
-  if (split_tokens(a.n))
+  if (split_tokens(a.n, kBwdBlocksPerSm))
     rc = a.rope.interleaved ? launch_backward<kWarps, true>(a, grid, stream)
                             : launch_backward<kWarps, false>(a, grid, stream);
   else

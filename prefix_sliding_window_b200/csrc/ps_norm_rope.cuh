@@ -221,23 +221,26 @@ __device__ __forceinline__ void lane_angles(const RopeLane& p, const float* cos,
   }
 }
 
-// What turns a lane's pairs of one token's q (or k) heads: with a norm the weights are in it, and
-// b is negative.
+// What turns a lane's pairs of one token's q (or k) heads: the weights are in it (ones where there
+// is no norm), and b is negative.
 struct RowCoef {
   float a[8], b[8], c[8], d[8];
 };
 template <bool INTER>
-__device__ __forceinline__ void row_coef(const RopeLane& p, bool norm, const float* w,
-                                         const float* cos, const float* sin, RowCoef& k) {
+__device__ __forceinline__ void row_coef(const RopeLane& p, const float* w, const float* cos,
+                                         const float* sin, RowCoef& k) {
   float c[8], s[8], wu[8], wv[8];
   lane_angles(p, cos, sin, c, s);
-  lane_weights<INTER>(w, p, wu, wv);  // (ones where there is no norm)
+  lane_weights<INTER>(w, p, wu, wv);
+  const uint64_t minus = pack_f32x2(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    k.a[i] = norm ? wu[i] * c[i] : c[i];
-    k.b[i] = norm ? -wv[i] * s[i] : s[i];
-    k.c[i] = norm ? wv[i] * c[i] : c[i];
-    k.d[i] = norm ? wu[i] * s[i] : s[i];
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t cc = pair_of(c, i), ss = pair_of(s, i);
+    const uint64_t u = pair_of(wu, i), v = pair_of(wv, i);
+    set_pair(k.a, i, fmul2(u, cc));
+    set_pair(k.b, i, fmul2(fmul2(v, ss), minus));
+    set_pair(k.c, i, fmul2(v, cc));
+    set_pair(k.d, i, fmul2(u, ss));
   }
 }
 
@@ -263,7 +266,7 @@ __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, cons
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < 4 ? p.rot1 : p.rot2) {
-        const float x = rope_lo(u[i], v[i], k.a[i], k.b[i]);
+        const float x = rope_lo(u[i], v[i], k.a[i], -k.b[i]);
         v[i] = rope_hi(u[i], v[i], k.c[i], k.d[i]);
         u[i] = x;
       }
