@@ -290,7 +290,7 @@ def make_norm(q_weight=None, k_weight=None, eps: float = 1e-6) -> PsQkNorm:
     norm = PsQkNorm(_ptr(q_weight), _ptr(k_weight),
                     types[given[0].dtype] if given else PS_TYPE_BF16, float(eps))
     norm.held = given  # the struct keeps only addresses
-    norm.device = given[0].device if given else None
+    norm.device = given[0].get_device() if given else None
     return norm
 
 
@@ -319,7 +319,7 @@ def make_cache_q4(prefix, ring, batch: int, block_table=None) -> PsKVCacheQ4:
             for part in (prefix, ring) for t in (part or (None,) * 3)]
     cache = PsKVCacheQ4(*ptrs, int(batch), _ptr(block_table), n_blocks, stride, 0)
     cache.held = held  # the struct keeps only addresses
-    cache.device = held[0].device if held else None
+    cache.device = held[0].get_device() if held else None
     return cache
 
 
@@ -499,62 +499,88 @@ def ps_masked_prefill_attn_bwd(params: PsParams, q, k, v, out, dout, lse, batch:
     _check(rc, "ps_masked_prefill_attn_bwd")
 
 
-def _tensor(name: str, t, dtype, device, numel: int):
-    """A contiguous CUDA tensor of the library's type and of at least numel elements."""
-    if t.dtype != dtype or t.device != device or t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous {dtype} of >= {numel} elements on {device} expected, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _tensor(name: str, t, dtype, device: int, numel: int):
+    """A contiguous tensor of the library's type and of at least numel elements on CUDA device
+    `device`."""
+    if t.dtype is not dtype or t.get_device() != device or t.numel() < numel or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} of >= {numel} elements on cuda:{device} "
+                         f"expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _heads(name: str, t, tokens: int, heads: int, device):
+def _heads(name: str, t, tokens: int, heads: int, device: int):
     """Rows of heads: [tokens, heads, 128] (or leading dims that flatten to tokens) with heads
     contiguous in a token.  Returns the address and the stride between tokens."""
-    import torch
     sh, st = t.shape, t.stride()
-    ok = (t.dtype == torch.bfloat16 and t.device == device and len(sh) >= 3 and sh[-1] == 128
-          and sh[-2] == heads and st[-1] == 1 and (st[-2] == 128 or heads == 1))
+    ok = (t.dtype is _torch().bfloat16 and t.get_device() == device and len(sh) >= 3
+          and sh[-1] == 128 and sh[-2] == heads and st[-1] == 1 and (st[-2] == 128 or heads == 1))
     n, stride = 1, heads * 128
     if ok:
         for size, step in zip(sh[-3::-1], st[-3::-1]):  # leading dims: evenly spaced tokens
-            if n == 1 and size != 1:
-                stride = step
-            ok = ok and (size == 1 or step == n * stride)
-            n *= size
+            if size != 1:
+                if n == 1:
+                    stride = step
+                ok = ok and step == n * stride
+                n *= size
         ok = ok and n == tokens
     if not ok:
-        raise ValueError(f"{name}: bf16 [{tokens}, {heads}, 128] with contiguous heads on {device} "
-                         f"expected, got {t.dtype} {tuple(sh)} strides {st} on {t.device}")
+        raise ValueError(f"{name}: bf16 [{tokens}, {heads}, 128] with contiguous heads on "
+                         f"cuda:{device} expected, got {t.dtype} {tuple(sh)} strides {st} on "
+                         f"{t.device}")
     return t.data_ptr(), stride
 
 
-def _device_of(pos, norm=None, cache=None):
-    """The device of a call: the current one, where everything it is given lives."""
-    import torch
-    dev = pos.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"positions are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _device_of(pos, norm=None, cache=None) -> int:
+    """The device index of a call: the current device, where everything it is given lives."""
+    dev = pos.get_device()
+    if dev < 0 or dev != _torch().cuda.current_device():
+        raise ValueError(f"positions are on {pos.device}, the current device is "
+                         f"cuda:{_torch().cuda.current_device()}")
     for what in (norm, cache):
         if what is not None and getattr(what, "device", None) not in (None, dev):
-            raise ValueError(f"weights or cache on {what.device}, positions on {dev}")
+            raise ValueError(f"weights or cache on cuda:{what.device}, positions on cuda:{dev}")
     return dev
 
 
-def _workspace(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _stream_on(stream, device: int):
+    """The stream's handle; None: the current stream of the device.  (Asked of the runtime by its
+    raw handle where torch offers that: building a Stream object takes longer than a launch.)"""
+    if stream is not None:
+        return _stream(stream)
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else _stream(None)
 
 
-def _status_ptr(t, device):
-    import torch
-    return None if t is None else _tensor("dev_status", t, torch.int32, device, 1)
+def _workspace(ws, device: int):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{device} expected, got one on "
+                         f"{ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _status_ptr(t, device: int):
+    return None if t is None else _tensor("dev_status", t, _torch().int32, device, 1)
 
 
 def ps_qk_norm_rope(params: PsParams, rope: PsRope, norm, q, k, pos, q_out, k_out,
                     dev_status=None, stream=None) -> None:
     """Head norm (norm None: none) and rotation of q [N, Hq, 128] and k [N, Hkv, 128] (views of
     packed rows allowed; either None with its output) at pos [N]."""
-    import torch
+    torch = _torch()
     dev = _device_of(pos, norm)
     n = pos.numel()
     hq, hkv = params.n_q_heads, params.n_kv_heads
@@ -568,7 +594,7 @@ def ps_qk_norm_rope(params: PsParams, rope: PsRope, norm, q, k, pos, q_out, k_ou
         ko = _tensor("k_out", k_out, torch.bfloat16, dev, n * hkv * 128)
     rc = load().ps_qk_norm_rope(params, rope, norm, qp, qs, kp, ks,
                                 _tensor("pos", pos, torch.int64, dev, n), n, qo, ko,
-                                _status_ptr(dev_status, dev), _stream(stream))
+                                _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_qk_norm_rope")
 
 
@@ -581,7 +607,7 @@ def ps_qk_norm_rope_bwd(params: PsParams, rope: PsRope, norm, q, k, pos, dq_out,
                         stream=None) -> None:
     """Gradients of ps_qk_norm_rope: dq, dk (views of packed rows allowed) and, where given, the
     weights' (fp32 [128])."""
-    import torch
+    torch = _torch()
     dev = _device_of(pos, norm)
     n = pos.numel()
     hq, hkv = params.n_q_heads, params.n_kv_heads
@@ -599,16 +625,16 @@ def ps_qk_norm_rope_bwd(params: PsParams, rope: PsRope, norm, q, k, pos, dq_out,
         dkp, dks = _heads("dk", dk, n, hkv, dev)
     dwq = None if dq_weight is None else _tensor("dq_weight", dq_weight, torch.float32, dev, 128)
     dwk = None if dk_weight is None else _tensor("dk_weight", dk_weight, torch.float32, dev, 128)
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(workspace, dev)
     rc = load().ps_qk_norm_rope_bwd(params, rope, norm, qp, qs, kp, ks,
                                     _tensor("pos", pos, torch.int64, dev, n), n, gq, gk, dqp, dqs,
                                     dkp, dks, dwq, dwk, ws, ws_bytes,
-                                    _status_ptr(dev_status, dev), _stream(stream))
+                                    _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_qk_norm_rope_bwd")
 
 
 def _append_rows(params, batch, k_new, v_new, q, q_out, pos0, T, dev):
-    import torch
+    torch = _torch()
     n = int(batch) * int(T)
     kp, ks = _heads("k_new", k_new, n, params.n_kv_heads, dev)
     vp, vs = _heads("v_new", v_new, n, params.n_kv_heads, dev)
@@ -627,7 +653,7 @@ def ps_kv_append_norm_rope(params: PsParams, rope: PsRope, norm, cache: PsKVCach
     rc = load().ps_kv_append_norm_rope(params, rope, norm, cache,
                                        *_append_rows(params, cache.batch, k_new, v_new, q, q_out,
                                                      pos0, T, dev),
-                                       _status_ptr(dev_status, dev), _stream(stream))
+                                       _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_kv_append_norm_rope")
 
 
@@ -635,7 +661,7 @@ def ps_kv_append_norm_rope_paged(params: PsParams, rope: PsRope, norm, k_pool, v
                                  block_table, batch: int, k_new, v_new, q, q_out, pos0, T: int,
                                  dev_status=None, stream=None) -> None:
     """The same into a paged store: pools [n_blocks, Hkv, 64, 128], block_table [batch, stride]."""
-    import torch
+    torch = _torch()
     dev = _device_of(pos0, norm)
     blocks = int(k_pool.shape[0])
     rows = blocks * params.n_kv_heads * 64 * 128
@@ -645,7 +671,7 @@ def ps_kv_append_norm_rope_paged(params: PsParams, rope: PsRope, norm, k_pool, v
         _tensor("block_table", block_table, torch.int32, dev, batch * block_table.shape[1]),
         int(block_table.shape[1]), int(batch),
         *_append_rows(params, batch, k_new, v_new, q, q_out, pos0, T, dev),
-        _status_ptr(dev_status, dev), _stream(stream))
+        _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_kv_append_norm_rope_paged")
 
 
@@ -657,20 +683,20 @@ def ps_kv_append_norm_rope_q4(params: PsParams, rope: PsRope, norm, cache: PsKVC
     rc = load().ps_kv_append_norm_rope_q4(params, rope, norm, cache,
                                           *_append_rows(params, cache.batch, k_new, v_new, q,
                                                         q_out, pos0, T, dev),
-                                          _status_ptr(dev_status, dev), _stream(stream))
+                                          _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_kv_append_norm_rope_q4")
 
 
 def ps_kv_read_q4(params: PsParams, cache: PsKVCacheQ4, pos0, T: int, k_out, v_out,
                   dev_status=None, stream=None) -> None:
     """Rows of positions [pos0, pos0 + T) of a 4-bit store as bf16 [batch, T, Hkv, 128]."""
-    import torch
+    torch = _torch()
     dev = _device_of(pos0, None, cache)
     n = cache.batch * int(T) * params.n_kv_heads * 128
     out = [None if t is None else _tensor(name, t, torch.bfloat16, dev, n)
            for name, t in (("k_out", k_out), ("v_out", v_out))]
     rc = load().ps_kv_read_q4(params, cache, _tensor("pos0", pos0, torch.int64, dev, cache.batch),
-                              int(T), *out, _status_ptr(dev_status, dev), _stream(stream))
+                              int(T), *out, _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_kv_read_q4")
 
 
@@ -681,16 +707,16 @@ def ps_decode_q4_workspace_bytes(params: PsParams, batch: int) -> int:
 def ps_decode_attn_q4(params: PsParams, cache: PsKVCacheQ4, q, pos, out, lse=None, workspace=None,
                       dev_status=None, stream=None) -> None:
     """ps_decode_attn over a 4-bit store."""
-    import torch
+    torch = _torch()
     dev = _device_of(pos, None, cache)
     rows = cache.batch * params.n_q_heads
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(workspace, dev)
     rc = load().ps_decode_attn_q4(
         params, cache, _tensor("q", q, torch.bfloat16, dev, rows * 128),
         _tensor("pos", pos, torch.int64, dev, cache.batch),
         _tensor("out", out, torch.bfloat16, dev, rows * 128),
         None if lse is None else _tensor("lse", lse, torch.float32, dev, rows), ws, ws_bytes,
-        _status_ptr(dev_status, dev), _stream(stream))
+        _status_ptr(dev_status, dev), _stream_on(stream, dev))
     _check(rc, "ps_decode_attn_q4")
 
 
