@@ -6,14 +6,16 @@
 //   o_d = sum_k p_k m_kg + sum_k (p_k s_kg) u_kd,  p = softmax(scale S)
 // A row is 144 bytes (64 of K, 64 of V, 16 of scales and minima), so the kernel is bound by HBM
 // once the codes can be fed to the tensor cores cheaply:
-//  * a code u enters the matrix product as a bf16 subnormal: four bits at the bottom of a half
-//    word are u 2^-133 and the next four, masked in place, 16 u 2^-133 (exact: the exponent field
-//    stays 0 or 1, which share a spacing; the tensor cores take subnormals in full).  A word of
-//    eight K codes costs one shift and four ands, of V codes four byte moves and six ands.
-//    Queries and weights carry a factor 2^64 against the small codes, taken off with the 2^-133
-//    and the 16s after the sums.  (As e4m3 bytes, u 2^-9, a word would cost three operations, but
-//    there is no such warp product in hardware: it is unpacked to halves, 186 us where this
-//    takes 139 at 256 sequences of 28 / 4 heads)
+//  * a code u enters the matrix products as a subnormal: four bits at the bottom of a half word
+//    are u 2^-133 as bf16 and u 2^-24 as fp16, the next four, masked in place, 16 times that
+//    (exactly: the codes stay where the spacing is the subnormals'; the tensor cores take
+//    subnormals in full).  A word of eight codes costs one shift and four ands, V's one byte move
+//    more to bring two rows together.  (As e4m3 bytes a word would cost three operations, but there is no
+//    such warp product in hardware: it is unpacked to halves, 186 us where this takes 139 at 256
+//    sequences of 28 / 4 heads)
+//  * queries are bf16 as given, times 2^64 against the small codes; weights are fp16, on a scale
+//    that keeps the greatest weight times V scale in [2^6, 2^14): 11 bits down to 2^-20 of the
+//    greatest.  (As bf16 their 8 bits tripled the output's error, since codes are not centred)
 //  * the dims of a row are stored so that one 16-byte load gives a lane the words of a whole
 //    K fragment row; which dim goes to which position of the product does not matter as long as
 //    the query's fragment agrees
@@ -53,10 +55,13 @@ constexpr int kMinRowsPerBlock = kSmWarps * kTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxBatch = 1024;
-// queries and weights carry 2^64 against the subnormal codes
-constexpr float kLiftLog2 = 64.f;
-constexpr float kLift = 18446744073709551616.f;     // 2^64
+constexpr float kLift = 18446744073709551616.f;     // 2^64: queries, against the codes' 2^-133
 constexpr float kUncode = 590295810358705651712.f;  // 2^69 = 2^133 / 2^64
+constexpr float kUncodeV = 16777216.f;              // 2^24
+// A weight times its row's V scale is below 2^(kWeightLog2 + kMaxSlack) = 2^14 < 65504.
+constexpr int kWeightLog2 = 6;
+// V scales below 2^kLeastScale are taken as that (fp32 sums of weights over them stay finite).
+constexpr int kLeastScale = -90;
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
 constexpr float kMaxSlack = 8.f;
@@ -232,18 +237,35 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two floats as an fp16 pair, the first in the low half.
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// The greater of each 16-bit half.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-// Codes as bf16 pairs, one from each half word, of a byte's two: the lower one, the upper one
-// (16 u), or both together (u + 16 u', still on the subnormals' spacing); the high byte moved down.
+// Codes as pairs of small floats, one from each half word, of the low byte's two: the lower one,
+// and the upper one (16 u).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t w) { return w & 0x000f000fu; }
-__device__ __forceinline__ uint32_t pair_byte(uint32_t w) { return w & 0x00ff00ffu; }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t w) { return w & 0x00f000f0u; }
-__device__ __forceinline__ uint32_t pair_byte1(uint32_t w) { return __byte_perm(w, 0, 0x4341); }
 
 // The halves of a word of two bf16 as floats: adding -0 in mixed precision, which the FMA pipe
 // does, where a shift or a mask would take the integer pipe that the codes are unpacked on.
@@ -433,8 +455,10 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
     st.mn[0][0] = st.mn[0][1] = st.mn[1][0] = st.mn[1][1] = 0.f;
     // a score (before c) above this moves the running maximum m
     float above[2] = {-INFINITY, -INFINITY};
-    // weights are 2^(c x + shift), shift = 64 - m (while there is no m, no score counts)
+    // weights are 2^(c x + shift), shift = kWeightLog2 - m - log2 of the least power of two above
+    // every V scale so far (while there is no m, no score counts)
     float shift[2] = {INFINITY, INFINITY};
+    int scale_exp = kLeastScale;
 
     const int kr = tile_row(g8);  // this lane's K rows: kr, kr + 8
     for (uint32_t first = warp * kTile; first < piece; first += kWarps * kTile) {
@@ -496,16 +520,27 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         mx[e] = fmaxf(max3f(x[0][e], x[0][2 + e], x[1][e]), x[1][2 + e]);
-      if (__any_sync(0xffffffffu, mx[0] > above[0] || mx[1] > above[1])) {
+      // this lane looks at row `lane`'s V scales (bf16, not negative: they compare as integers)
+      const uint2 own = *reinterpret_cast<const uint2*>(stage + 2 * kTile * kQ4RowBytes +
+                                                        lane * kQ4RecordBytes + 8);
+      const uint32_t top = max_u16x2(own.x, own.y) & 0xffffu;
+      if (__any_sync(0xffffffffu, mx[0] > above[0] || mx[1] > above[1] ||
+                                      top >= static_cast<uint32_t>(scale_exp + 127) << 7)) {
+        // (a scale that is not finite makes its products NaN whatever the exponent)
+        const uint32_t most = __reduce_max_sync(0xffffffffu, top < 0x7f80u ? top : 0u);
+        const int was = scale_exp;
+        scale_exp = max(scale_exp, static_cast<int>(most >> 7) - 126);
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-          const float to = fminf(shift[e], kLiftLog2 - mx[e] * c);
+          // the old m, from the old shift (-inf where there is none)
+          const float m = fmaxf(static_cast<float>(kWeightLog2 - was) - shift[e], mx[e] * c);
+          const float to = static_cast<float>(kWeightLog2 - scale_exp) - m;
           f[e] = shift[e] == INFINITY ? 0.f : fast_exp2(to - shift[e]);
-          if (to != INFINITY) above[e] = (kLiftLog2 + kMaxSlack - to) / c;
+          if (m != -INFINITY) above[e] = (m + kMaxSlack) / c;
           shift[e] = to;
           st.l[e] *= f[e];
           st.mn[0][e] *= f[e];
@@ -540,26 +575,20 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const uint32_t k0 = g ? c0.y : c0.x, k1 = g ? c1.y : c1.x;
-          // a weight times its row's scale, rounded to bf16: the tensor cores' operand type
-          const uint32_t b0 = transpose8(cvt_bf16x2(p[0] * lo_f(k0), p[1] * lo_f(k0)));
-          const uint32_t b1 = transpose8(cvt_bf16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
+          // a weight times its row's scale, rounded to fp16: the tensor cores' operand type
+          const uint32_t b0 = transpose8(cvt_f16x2(p[0] * lo_f(k0), p[1] * lo_f(k0)));
+          const uint32_t b1 = transpose8(cvt_f16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
           st.mn[g][0] = fmaf(p[0], hi_f(k0), fmaf(p[2], hi_f(k1), st.mn[g][0]));
           st.mn[g][1] = fmaf(p[1], hi_f(k0), fmaf(p[3], hi_f(k1), st.mn[g][1]));
           const uint32_t x0 = g ? v0.y : v0.x, x1 = g ? v1.y : v1.x;
           const uint32_t x2 = g ? v2.y : v2.x, x3 = g ? v3.y : v3.x;
           const uint32_t e0 = __byte_perm(x0, x1, 0x5410), f0 = __byte_perm(x0, x1, 0x7632);
           const uint32_t e1 = __byte_perm(x2, x3, 0x5410), f1 = __byte_perm(x2, x3, 0x7632);
-          // even tiles take a byte, u + 16 u', odd ones its 16 u': one mask less a byte, and
-          // the even sums are told apart at the end
-          mma(st.o[4 * g + 0], pair_byte(e0), pair_byte(f0), pair_byte(e1),
-                         pair_byte(f1), b0, b1);
-          mma(st.o[4 * g + 1], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0,
-                         b1);
-          const uint32_t e2 = pair_byte1(e0), f2 = pair_byte1(f0);
-          const uint32_t e3 = pair_byte1(e1), f3 = pair_byte1(f1);
-          mma(st.o[4 * g + 2], e2, f2, e3, f3, b0, b1);
-          mma(st.o[4 * g + 3], pair_hi(e2), pair_hi(f2), pair_hi(e3), pair_hi(f3), b0,
-                         b1);
+          mma_f16(st.o[4 * g + 0], pair_lo(e0), pair_lo(f0), pair_lo(e1), pair_lo(f1), b0, b1);
+          mma_f16(st.o[4 * g + 1], pair_hi(e0), pair_hi(f0), pair_hi(e1), pair_hi(f1), b0, b1);
+          const uint32_t e2 = e0 >> 8, f2 = f0 >> 8, e3 = e1 >> 8, f3 = f1 >> 8;
+          mma_f16(st.o[4 * g + 2], pair_lo(e2), pair_lo(f2), pair_lo(e3), pair_lo(f3), b0, b1);
+          mma_f16(st.o[4 * g + 3], pair_hi(e2), pair_hi(f2), pair_hi(e3), pair_hi(f3), b0, b1);
         }
       }
       __syncwarp();  // every lane has read the stage
@@ -578,8 +607,8 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
     }
 
     // ------------------------------------------------ combine the warps, write the piece
-    // the stage to be filled next holds the warp's result now, [8 heads][128], then m[8], l[8], all
-    // but m times 2^64; the other stages may hold the next piece's first tiles
+    // the stage to be filled next holds the warp's result now, [8 heads][128], then m[8], l[8], o
+    // and l to be taken times 2^m; the other stages may hold the next piece's first tiles
     float* res = reinterpret_cast<float*>(smem + warp * kWarpBytes + in);
     if (lane == 0) s_result[warp] = res;
 #pragma unroll
@@ -597,14 +626,13 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
           const int i = 4 * g + (d >> 1), j = 2 * (d & 1) + e;
-          const float o = (d & 2) ? st.o[i][j] * (1.f / 16.f) : st.o[i][j] - st.o[i | 1][j];
-          y[d] = fmaf(o * kLift, kUncode, st.mn[g][e]);  // times 2^133
+          y[d] = fmaf(st.o[i][j], (d & 2) ? kUncodeV / 16.f : kUncodeV, st.mn[g][e]);
         }
         reinterpret_cast<float4*>(dst + 64 * g)[0] = make_float4(y[0], y[1], y[2], y[3]);
         reinterpret_cast<float4*>(dst + 64 * g)[1] = make_float4(y[4], y[5], y[6], y[7]);
       }
       if (g8 == 0) {
-        res[kMaxGroup * kHeadDim + 2 * t4 + e] = kLiftLog2 - shift[e];
+        res[kMaxGroup * kHeadDim + 2 * t4 + e] = -shift[e];
         res[kMaxGroup * kHeadDim + kMaxGroup + 2 * t4 + e] = st.l[e];
       }
     }
@@ -631,7 +659,7 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps / kWarps)
         acc.w = fmaf(f, y.w, acc.w);
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      const float lse2 = L == 0.f ? -INFINITY : M + log2f(L * (1.f / kLift));
+      const float lse2 = L == 0.f ? -INFINITY : M + log2f(L);
       acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
       if (piece < s_piece[warp][cur].n) {
         const int64_t slot = (2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1)) * kMaxGroup + head;

@@ -3,15 +3,16 @@
 Written rows are compared bit for bit: the quantiser works on the bf16 row that the bf16 append
 stores, in correctly rounded fp32 steps.  Read rows too (m + s u, one fma, one rounding).
 
-Decode tolerances (before the first run), per output element, with p the exact weights:
+Decode tolerances, per output element, with p the exact weights:
   2^-8 |o|                 the output's rounding to bf16
-  2^-8 sum p s u           each weight times a row's scale is rounded to bf16 once (a code enters
-                           the product exactly; the offset it carries is taken off with the same
-                           rounded weights)
-  2^-15 sum p s 143        fp32 accumulation of codes offset by 128, up to ~2^9 roundings of 2^-24
+  2^-11 sum p s u          each weight times a row's scale is rounded to fp16 once (codes enter the
+                           products exactly)
+  n 2^-30 max p max s 15   weights below 2^-20 of the greatest are fp16 subnormals: off by half a
+                           spacing, 2^-25, where the greatest is 2^5 or more
+  2^-15 sum p s 15         fp32 accumulation, up to ~2^9 roundings of 2^-24
   2 E sum p |v|            scores off by at most E change a weight by a factor e^(+-2E)
-with E = scale 2^-19 sum_g s_g 143 sum_d |q_d| (the score's fp32 sum of offset codes: 32 roundings)
-and lse within E + 2^-20 max(1, |lse|).
+with E = scale 2^-19 sum_g s_g 15 sum_d |q_d| (the score's fp32 sum of codes: 32 roundings) + the
+same of the minima, 2^-21 scale sum_g |m_g sum_d q_d|, and lse within E + 2^-20 max(1, |lse|).
 """
 import math
 
@@ -84,10 +85,15 @@ def _check_decode(params, q, out, lse, rows_of, what):
             p = e / z
             want, want_l = p @ v[:, h], top + math.log(z)
             aq = np.abs(qv[b, head]).reshape(2, 64).sum(-1)
-            E = scale * 2.0 ** -19 * 143 * (sk[:, h, :, 0] @ aq).max()
+            Qg = np.abs(qv[b, head].reshape(2, 64).sum(-1))
+            least = k[:, h].reshape(-1, 2, 64).min(-1)   # m + s u >= m, so |m| <= |least| + 15 s
+            E = scale * (2.0 ** -19 * 15 * (sk[:, h, :, 0] @ aq)
+                         + 2.0 ** -21 * ((np.abs(least) + 15 * sk[:, h, :, 0]) @ Qg)).max()
             su = (sv[:, h] * u[:, h]).reshape(-1, 128)
-            tol = 2.0 ** -8 * (np.abs(want) + p @ su) \
-                + 2.0 ** -15 * 143 * np.repeat(p @ sv[:, h, :, 0], 64) + 2 * E * (p @ np.abs(v[:, h]))
+            s1 = sv[:, h, :, 0]
+            tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * (p @ su) \
+                + len(p) * 2.0 ** -30 * p.max() * s1.max() * 15 \
+                + 2.0 ** -15 * 15 * np.repeat(p @ s1, 64) + 2 * E * (p @ np.abs(v[:, h]))
             bad = ~(np.abs(got[b, head] - want) <= tol)
             assert not bad.any(), (what, b, head, int(bad.sum()),
                                    np.abs(got[b, head] - want).max())
