@@ -5,7 +5,8 @@
 // that the two dims of every rotated pair sit in one lane.  Rotation then needs no exchange, the
 // norm's sum of squares three shuffles, and a warp's loads are whole 128-byte half rows.
 //   half layout, R rotated dims, m = R / 16: lanes l < m hold chunks (l, l + m), dims (i, i + R/2);
-//     the unrotated chunks 2m .. 15 go two by two to the other lanes
+//     the unrotated chunks 2m .. 15 go to the other lanes, first halves then second, so that a
+//     warp's loads cover whole sectors (neighbouring chunks to one lane: 138 us where this takes XX)
 //   interleaved: chunks (l, l + 8); pairs (2i, 2i + 1) never leave a chunk
 // A warp takes four heads of one token at a time; q and k heads are never mixed in one item.
 //
@@ -46,8 +47,8 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   } else {
     const int m = r.dim / 16;
     p.rot1 = p.rot2 = l < m;
-    p.c1 = l < m ? l : 2 * l;  // 2 m + 2 (l - m)
-    p.c2 = l < m ? l + m : 2 * l + 1;
+    p.c1 = l < m ? l : l + m;  // 2 m + (l - m), and 8 - m chunks on
+    p.c2 = l < m ? l + m : l + 8;
     p.a1 = 8 * l;
     p.a2 = 8 * l + 4;
   }
@@ -92,13 +93,41 @@ __device__ __forceinline__ void pack_pairs(const float (&u)[8], const float (&v)
   }
 }
 
-// One warp forms all angles of a token, range reduction in 64 bits (rope_cos_sin), into its own
-// cos[64], sin[64] in shared memory.
+// cos and sin of p * inv_f: reduced to [-pi/4, pi/4] in float64 (pi/2 in two parts; the first
+// difference is exact, so the remainder is good to 2^-53 of pi/2 beside the product's own rounding),
+// then Taylor sums in fp32, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9) before roundings.
+// 30 instructions where the library's other rotations, through sincosf, take 240: with 16 + 2
+// heads a token's 64 angles were a fifth of the forward's time (73 us at 32768 tokens, now XXX).
+__device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
+  const double ang = p * inv_f;
+  const double shifter = 6755399441055744.0;  // 1.5 2^52: the sum's low word holds the integer
+  const double t = fma(ang, 0.63661977236758134308, shifter);
+  const int quadrant = __double2loint(t);
+  const double k = t - shifter;
+  double red = fma(-k, 1.5707963267948965580, ang);
+  red = fma(-k, 6.1232339957367660359e-17, red);
+  const float r = static_cast<float>(red), r2 = r * r;
+  float s = fmaf(r2, 1.f / 362880.f, -1.f / 5040.f);
+  s = fmaf(s, r2, 1.f / 120.f);
+  s = fmaf(s, r2, -1.f / 6.f);
+  s = fmaf(s, r * r2, r);
+  float c = fmaf(r2, -1.f / 3628800.f, 1.f / 40320.f);
+  c = fmaf(c, r2, -1.f / 720.f);
+  c = fmaf(c, r2, 1.f / 24.f);
+  c = fmaf(c, r2, -0.5f);
+  c = fmaf(c, r2, 1.f);
+  const float x = (quadrant & 1) ? -s : c, y = (quadrant & 1) ? c : s;
+  return (quadrant & 2) ? make_float2(-x, -y) : make_float2(x, y);
+}
+
+// One warp forms all angles of a token, into its own cos[64], sin[64] in shared memory.
 __device__ __forceinline__ void rope_angles(const RopeArgs& r, int64_t pos, int lane, float* cos,
                                             float* sin) {
   __syncwarp();  // the last token's are no longer read
-  for (int i = lane; i < r.dim / 2; i += 32) {
-    const float2 cs = rope_cos_sin(double(pos), r.inv_freq[i]);
+#pragma unroll
+  for (int i = lane; i < kHalfDim; i += 32) {
+    if (i >= r.dim / 2) break;
+    const float2 cs = cos_sin_of(double(pos), r.inv_freq[i]);
     cos[i] = cs.x * r.attn;
     sin[i] = cs.y * r.attn;
   }
@@ -244,8 +273,7 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, const float* w, cons
   }
 }
 
-// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.  Without a norm the products
-// are rounded as everywhere else that the library rotates, so such rows are bit-identical.
+// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.
 __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, const RowCoef& k,
                                               float eps, float (&u)[8], float (&v)[8]) {
   if (norm) {
