@@ -59,8 +59,12 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 // Quantises a row held by eight lanes (chunks p.c1, p.c2 of a lane, bf16) and writes it: payload
 // words at `pay`, (s, m) of both groups at `rec` (8 bytes).  All lanes take part; only `live` ones
-// write.  A code is the rounded quotient (x - m) / s; the product with 1 / s is within 2e-6 of it,
-// so only a product that near to a half needs the division.
+// write.
+//
+// A code is (x - m) / s rounded to nearest even, by a product with 1 / s (within 2e-6 of the
+// quotient) and the remainder r = (x - m) - u s, which one fma gives exactly: beyond s / 2, or at
+// s / 2 with u odd, the code is one further on.  (On the bf16 grid such ties are common: dividing
+// where a product was near one ran for nearly every warp.)
 __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1, const uint4& r2,
                                              bool live, int lane8, uint8_t* pay, uint8_t* rec) {
   float x[2][8], lo[2], hi[2];
@@ -93,35 +97,35 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
     const int g = chunk >> 3, b = chunk & 7;
     const float mm = g ? m[1] : m[0], ss = g ? s[1] : s[0];
     const float inv = __fdiv_rn(1.f, ss);
-    float u[8], off = 0.f;
+    const uint32_t half = __float_as_uint(0.5f * ss);
+    float u[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = __fmul_rn(__fsub_rn(x[c][e], mm), inv);
-      u[e] = __fsub_rn(__fadd_rn(t, round), round);
-      off = max_nan(off, fabsf(__fsub_rn(t, u[e])));
+      const float d = __fsub_rn(x[c][e], mm);
+      const float t = fmaf(d, inv, round);
+      u[e] = t - round;
+      const float r = fmaf(-u[e], ss, d);
+      // an odd code leaves at the border already: its bound is the float below s / 2
+      const float bound = __uint_as_float(half - (__float_as_uint(t) & 1u));
+      if (fabsf(r) > bound) u[e] += copysignf(1.f, r);
+      u[e] = fminf(u[e], 15.f);
     }
-    if (!(off < 0.499996f)) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = 0.f;
-      if (ss > 0.f) {
+    if (ss > 0.f && ss < 1e-37f) {  // 1 / s overflows below 2^-128
 #pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const float q = rintf(__fdiv_rn(x[c][e] - mm, ss));
+      for (int e = 0; e < 8; ++e) {
+        const float q = fminf(rintf(__fdiv_rn(x[c][e] - mm, ss)), 15.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i == e) u[i] = q;
-        }
+        for (int i = 0; i < 8; ++i)
+          if (i == e) u[i] = q;
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] = fminf(u[e], 15.f);
     // halves of the word as sums of codes times 16^i, exact in fp32; 2^23 puts them into the
     // low mantissa bits
     const float lo16 = fmaf(u[6], 4096.f, fmaf(u[4], 256.f, fmaf(u[2], 16.f, u[0] + 8388608.f)));
     const float hi16 = fmaf(u[7], 4096.f, fmaf(u[5], 256.f, fmaf(u[3], 16.f, u[1] + 8388608.f)));
-    if (live)
-      *reinterpret_cast<uint32_t*>(pay + 4 * (2 * b + g)) =
-          __byte_perm(__float_as_uint(lo16), __float_as_uint(hi16), 0x5410);
+    const uint32_t word = __byte_perm(__float_as_uint(lo16), __float_as_uint(hi16), 0x5410);
+    // (s is 0 or not a number: codes of 0)
+    if (live) *reinterpret_cast<uint32_t*>(pay + 4 * (2 * b + g)) = ss > 0.f ? word : 0u;
   }
   if (live && lane8 == 0)
     *reinterpret_cast<uint2*>(rec) =
@@ -152,33 +156,48 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   pdl_trigger();
 
   const int64_t end = items.any() ? a.batch * a.T : 0;
-  // where a token's rows go; flag set or stale: nowhere (stale: a newer token of the call owns the
+  // a token's sequence and place in it move on without divisions
+  const int64_t step_b = items.step / a.T;
+  const int32_t step_t = static_cast<int32_t>(items.step - step_b * a.T);
+  struct Place {
+    int64_t b;
+    int32_t t;
+  };
+  auto next_place = [&](Place& g) {
+    g.b += step_b;
+    g.t += step_t;
+    if (g.t >= a.T) g.t -= a.T, ++g.b;
+  };
+  // where a token's rows go; `writes`: they go anywhere (a newer token of the call may own the
   // ring slot)
   struct Token {
     int64_t pos;
     StoreRow row;
-    bool stale;
+    bool writes;
   };
-  auto token = [&](int64_t tok) {
-    const int64_t b = tok < (int64_t(1) << 32) ? uint32_t(tok) / uint32_t(a.T) : tok / a.T;
-    const int64_t p0 = a.pos0[b];
+  auto token = [&](const Place& g) {
+    const int64_t p0 = a.pos0[g.b];
     Token t;
-    t.pos = p0 + (tok - b * a.T);
-    t.row = store_row(a.store, a.hkv, b, t.pos);
-    t.stale = !a.store.linear && t.pos >= a.store.lp && t.pos <= p0 + a.T - 1 - a.store.w;
+    t.pos = p0 + g.t;
+    t.row = store_row(a.store, a.hkv, g.b, t.pos);
+    const bool stale =
+        !a.store.linear && t.pos >= a.store.lp && t.pos <= p0 + a.T - 1 - a.store.w;
+    t.writes = !t.row.flag && !stale;
     return t;
   };
-  // past the K and V segments of tokens that write none
-  auto settle = [&](Segment& g, bool flag) {
-    while (g.tok < end && g.is_k) {
-      const Token t = token(g.tok);
-      if (flag && t.row.flag && a.status && lane == 0) atomicOr(a.status, t.row.flag);
-      if (!t.row.flag && !t.stale) break;
-      g = items.first(g.tok + items.step);
+  Segment at = items.first(gw / SPLIT), far = at;
+  Place at_place, far_place;
+  at_place.b = at.tok / a.T;
+  at_place.t = static_cast<int32_t>(at.tok - at_place.b * a.T);
+  far_place = at_place;
+  // moves `far` past the K and V segments of tokens that write none
+  auto settle_far = [&]() {
+    while (far.tok < end && far.is_k && !token(far_place).writes) {
+      far = items.first(far.tok + items.step);
+      next_place(far_place);
     }
   };
-  Segment at = items.first(gw / SPLIT), far = at;
-  settle(far, false);
+  settle_far();
   const __nv_bfloat16* src = nullptr;  // the next q item's
   auto open = [&]() {
     if (!far.is_k) src = a.q + far.tok * a.q_stride + items.q0 * 4 * kHeadDim + o1;
@@ -202,8 +221,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       copy16_if(ring + in + kItem / 2, from + d2, there);
       in = in == kRing - kItem ? 0 : in + kItem;
       src += items.kStride;
+      const int64_t was = far.tok;
       if (items.next(far)) {
-        settle(far, false);
+        if (far.tok != was) next_place(far_place);
+        settle_far();
         open();
       }
     }
@@ -216,25 +237,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
   RowCoef coef;
   int64_t tok = -1;  // whose angles are in shared memory
-  bool fresh = true, skip = false;
+  bool fresh = true, skip = false, writes = false;
   StoreRow place{0, 0, 0, 0};
   __nv_bfloat16* dst = nullptr;
   uint32_t out = 0;
-  settle(at, true);
   while (at.tok < end) {
     const bool kv = at.is_k;
     const bool norm = (kv ? a.norm.wk : a.norm.wq) != nullptr;
     if (fresh) {
       if (at.tok != tok) {
         tok = at.tok;
-        const Token t = token(tok);
+        const Token t = token(at_place);
         if (t.row.flag && a.status && lane == 0) atomicOr(a.status, t.row.flag);
         // a token the store has no place for is skipped, its queries become zeros; a bad table
         // entry only loses the row
         const bool bad = bad_rope_position(t.pos);
         skip = bad || (t.row.flag && !a.store.table);
         place = t.row;
-        rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+        writes = t.writes;
+        if (!kv || writes)
+          rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+      }
+      if (kv && !writes) {  // on to the next token
+        at = items.first(tok + items.step);
+        next_place(at_place);
+        continue;
       }
       row_coef<INTER>(p, s_w + (kv ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
       if (!kv) dst = a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
@@ -272,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
     }
     fresh = items.next(at);
-    if (fresh) settle(at, true);
+    if (at.tok != tok) next_place(at_place);
   }
 }
 
