@@ -17,8 +17,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 3, kAhead = 4;  // items in flight a warp, forward
-constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 3;  // backward: an item is twice the bytes
+constexpr int kBlocksPerSm = 2, kAhead = 4;  // items in flight a warp, forward
+constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 2;  // backward: an item is twice the bytes
 
 // Warps stride over tokens; SPLIT of them share one (1 or 8) and take its items in turn.
 template <int SPLIT, bool INTER>
