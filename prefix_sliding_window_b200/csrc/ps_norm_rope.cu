@@ -7,7 +7,10 @@
 // registers over all of its heads; the rows of the next items are in flight as asynchronous copies
 // into a ring of shared memory, every lane its own 16-byte chunks, so that the depth of the
 // prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
-// 28 + 4 heads, XXX with the ring).  With few tokens eight warps share one.
+// 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
+//
+// At 4 x 8192 tokens of 28 + 4 heads the forward takes 92 us (5.8 TB/s, 90 % of a copy's rate), the
+// backward 137 us (91 %).
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -279,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
 }
 
 // dw[d] = the blocks' partials added up in block order: 32 columns a block, eight threads a
-// column (every eighth partial), then those eight in order.
+// column (every eighth partial), then those eight in order.  (32 threads a column: 0.5 us
+// longer at 1021 tokens.)
 __global__ void __launch_bounds__(256)
     norm_rope_dw_kernel(const float* __restrict__ partial, int32_t rows, float* dwq, float* dwk) {
   pdl_wait();
@@ -300,8 +304,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Eight warps share a token while every token has a block of its own in one wave (1021 tokens, more
-// than that, took 9.5 us shared and XXX one warp each).
+// Eight warps share a token while every token has a block of its own in one wave (16 + 2 heads, 296
+// tokens: 3.9 us shared, 5.5 one warp each; 1021 tokens: 8.2 and 5.6).
 bool split_tokens(int64_t n, int per_sm) { return n <= per_sm * (int64_t)sm_count(); }
 
 // One wave of blocks, or as many as there are tokens for.

@@ -6,7 +6,8 @@
 // norm's sum of squares three shuffles, and a warp's loads are whole 128-byte half rows.
 //   half layout, R rotated dims, m = R / 16: lanes l < m hold chunks (l, l + m), dims (i, i + R/2);
 //     the unrotated chunks 2m .. 15 go to the other lanes, first halves then second, so that a
-//     warp's loads cover whole sectors (neighbouring chunks to one lane: 138 us where this takes XX)
+//     warp's loads cover whole sectors (neighbouring chunks to one lane, nothing rotated: 138 us
+//     where this took 99)
 //   interleaved: chunks (l, l + 8); pairs (2i, 2i + 1) never leave a chunk
 // A warp takes four heads of one token at a time; q and k heads are never mixed in one item.
 //
@@ -94,10 +95,11 @@ __device__ __forceinline__ void pack_pairs(const float (&u)[8], const float (&v)
 }
 
 // cos and sin of p * inv_f: reduced to [-pi/4, pi/4] in float64 (pi/2 in two parts; the first
-// difference is exact, so the remainder is good to 2^-53 of pi/2 beside the product's own rounding),
-// then Taylor sums in fp32, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9) before roundings.
-// 30 instructions where the library's other rotations, through sincosf, take 240: with 16 + 2
-// heads a token's 64 angles were a fifth of the forward's time (73 us at 32768 tokens, now XXX).
+// difference is exact, so the remainder is good to 2^-53 of pi/2 beside the product's own
+// rounding), then Taylor sums in fp32, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9) before
+// roundings.  30 instructions where the library's other rotations, through sincosf, take 240: with
+// 16 + 2 heads a token's 64 angles were a fifth of the forward's time (73 us at 32768 tokens, 64
+// with these).
 __device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
   const double ang = p * inv_f;
   const double shifter = 6755399441055744.0;  // 1.5 2^52: the sum's low word holds the integer
