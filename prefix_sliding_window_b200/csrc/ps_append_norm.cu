@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         next_place(at_place);
         continue;
       }
-      row_coef<INTER>(p, s_w + (kv ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+      row_coef<INTER>(p, kv && norm, s_w + (kv ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
       if (!kv) dst = a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
     }
     load();
@@ -272,11 +272,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     out = out == kRing - kItem ? 0 : out + kItem;
     float u[8], v[8];
     unpack_pairs<INTER>(r1, r2, u, v);
-    norm_and_turn(p, norm, coef, a.norm.eps, u, v);
     uint4 y1, y2;
-    pack_pairs<INTER>(u, v, y1, y2);
     const bool live = row < at.rows;
     if (!kv) {
+      norm_and_turn(p, norm, false, coef, a.norm.eps, u, v);
+      pack_pairs<INTER>(u, v, y1, y2);
       if (skip) y1 = y2 = make_uint4(0, 0, 0, 0);
       if (live) {
         *reinterpret_cast<uint4*>(dst) = y1;
@@ -284,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
       dst += items.kStride;
     } else {
+      norm_and_turn(p, norm, true, coef, a.norm.eps, u, v);
+      pack_pairs<INTER>(u, v, y1, y2);
       const int r = 2 * a.hkv - at.rows + row;
       const bool is_v = r >= a.hkv;
       if (is_v) y1 = r1, y2 = r2;  // values as they are

@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
         if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
         rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
       }
-      row_coef<INTER>(p, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
+      row_coef<INTER>(p, at.is_k && norm, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp],
+                      s_sin[warp], coef);
       dst = at.is_k ? a.k_out + (tok * a.hkv + items.k0 * 4) * kHeadDim + o1
                     : a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
     }
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     const uint4* r = &s_ring[warp][0][0][lane] + out / sizeof(uint4);
     unpack_pairs<INTER>(r[0], r[32], u, v);
     out = out == kRing - kItem ? 0 : out + kItem;
-    norm_and_turn(p, norm, coef, a.norm.eps, u, v);
+    norm_and_turn(p, norm, at.is_k, coef, a.norm.eps, u, v);
     uint4 y1, y2;
     pack_pairs<INTER>(u, v, y1, y2);
     if (bad) y1 = y2 = make_uint4(0, 0, 0, 0);

@@ -11,10 +11,10 @@
 //   interleaved: chunks (l, l + 8); pairs (2i, 2i + 1) never leave a chunk
 // A warp takes four heads of one token at a time; q and k heads are never mixed in one item.
 //
-// A lane's eight pairs (u, v) become rstd (u a - v b), rstd (v c + u d) with coefficients that hold
-// the weights and the angles, a = w_u cos, b = w_v sin, c = w_v cos, d = w_u sin: formed once for
-// all heads of a token, they leave six operations a pair (340 -> 150 instructions per four heads
-// with the loads, where HBM allows 350).
+// A lane's eight pairs (u, v) of queries become rstd (u a - v b), rstd (v c + u d) with coefficients
+// that hold the weights and the angles, a = w_u cos, b = w_v sin, c = w_v cos, d = w_u sin: formed
+// once for all heads of a token, they leave six operations a pair (340 -> 150 instructions per four
+// heads with the loads, where HBM allows 350).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -189,6 +189,13 @@ __device__ __forceinline__ void set_pair(float (&x)[8], int i, uint64_t v) {
   x[2 * i + 1] = f.y;
 }
 
+// A product that is rounded by itself, whatever is done with it.
+__device__ __forceinline__ uint64_t fmul2_rn(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // 1 / sqrt(mean(x^2) + eps) of a row held by eight lanes, fp32.
 __device__ __forceinline__ float row_rstd(const float (&u)[8], const float (&v)[8], float eps) {
   uint64_t s = 0, t = 0;
@@ -252,14 +259,20 @@ __device__ __forceinline__ void lane_angles(const RopeLane& p, const float* cos,
   }
 }
 
-// What turns a lane's pairs of one token's q (or k) heads: the weights are in it (ones where there
-// is no norm), and b is negative.
+// What turns a lane's pairs of one token's heads.  Of queries: the weights (ones where there is no
+// norm) are in the angles, and b is negative.  Of normalised keys: a and c are the weights of u and
+// v, b and d cosines and sines.
 struct RowCoef {
   float a[8], b[8], c[8], d[8];
 };
 template <bool INTER>
-__device__ __forceinline__ void row_coef(const RopeLane& p, const float* w, const float* cos,
-                                         const float* sin, RowCoef& k) {
+__device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const float* w,
+                                         const float* cos, const float* sin, RowCoef& k) {
+  if (key) {
+    lane_angles(p, cos, sin, k.b, k.d);
+    lane_weights<INTER>(w, p, k.a, k.c);
+    return;
+  }
   float c[8], s[8], wu[8], wv[8];
   lane_angles(p, cos, sin, c, s);
   lane_weights<INTER>(w, p, wu, wv);
@@ -275,12 +288,33 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, const float* w, cons
   }
 }
 
-// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.
-__device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, const RowCoef& k,
-                                              float eps, float (&u)[8], float (&v)[8]) {
+// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.  Normalised keys (`key`) are
+// rounded step by step, x rstd, times w, the rotation's products and their sum, as the formula's
+// plain evaluation does: a 4-bit store turns a last bit that differs into a whole code now and then,
+// and a token has few key heads.
+__device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool key,
+                                              const RowCoef& k, float eps, float (&u)[8],
+                                              float (&v)[8]) {
   if (norm) {
     const float rstd = row_rstd(u, v, eps);
     const uint64_t r2 = pack_f32x2(rstd, rstd);
+    if (key) {
+      const uint64_t minus = pack_f32x2(-1.f, -1.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint64_t x = fmul2_rn(fmul2_rn(pair_of(u, i), r2), pair_of(k.a, i));
+        uint64_t y = fmul2_rn(fmul2_rn(pair_of(v, i), r2), pair_of(k.c, i));
+        if (i < 2 ? p.rot1 : p.rot2) {
+          const uint64_t c = pair_of(k.b, i), s = pair_of(k.d, i);
+          const uint64_t xs = fmul2_rn(x, s), ys = fmul2_rn(y, s);
+          x = ffma2(ys, minus, fmul2_rn(x, c));
+          y = fadd2(fmul2_rn(y, c), xs);
+        }
+        set_pair(u, i, x);
+        set_pair(v, i, y);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint64_t uu = pair_of(u, i), vv = pair_of(v, i);
