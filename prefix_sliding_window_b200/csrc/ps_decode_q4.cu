@@ -65,8 +65,9 @@ constexpr float kUncode = 590295810358705651712.f;  // 2^69 = 2^133 / 2^64
 constexpr float kUncodeV = 16777216.f;              // 2^24
 // A weight times its row's V scale is below 2^(kWeightLog2 + kMaxSlack) = 2^14 < 65504.
 constexpr int kWeightLog2 = 6;
-// V scales below 2^kLeastScale are taken as that (fp32 sums of weights over them stay finite).
-constexpr int kLeastScale = -90;
+// V scales below 2^kLeastScale count as that: weights stay below 2^74, and fp32 sums of them times
+// values finite, where all groups so far were constant (s = 0) and below 2^30.
+constexpr int kLeastScale = -60;
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
 constexpr float kMaxSlack = 8.f;

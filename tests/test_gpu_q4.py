@@ -176,6 +176,62 @@ def test_decode_one_long_among_short(cuda_device):
     _run_contiguous(cuda_device, 8, 2, 3000, 0, [2999, 0, 1, 2, 3, 4, 5])
 
 
+@pytest.mark.parametrize("hq,hkv,lp,positions", [
+    (2, 1, 70000, [69999]),                           # more pieces than a round of the merge
+    (4, 2, 5000, [4999, 0, 300, 4000, 31, 2047] * 4),  # a few pieces a unit, short ones among them
+    (8, 8, 9000, [8999, 1, 5000] * 8)])
+def test_decode_in_pieces(cuda_device, hq, hkv, lp, positions):
+    _run_contiguous(cuda_device, hq, hkv, lp, 0, positions, seed=lp)
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_decode_scales_of_all_sizes(cuda_device, back):
+    """V scales that jump by many powers of two from tile to tile, either way: constant groups,
+    2^-40, 2^-10, 1, 2^30; a query sees one more of these segments each."""
+    dev, hkv, hq, seg = cuda_device, 2, 6, 300
+    scales = [0.0, 2.0 ** -40, 2.0 ** -10, 1.0, 2.0 ** 30]
+    if back:
+        scales.reverse()
+    n = seg * len(scales)
+    one = _random_store(1, hkv, n, 77, dev)
+    g = torch.Generator(device=dev).manual_seed(78)
+    rec = one[2].view(1, hkv, n, 4, 2)
+    for i, s in enumerate(scales):
+        x = rec[:, :, i * seg:(i + 1) * seg, 2:]
+        x[..., 0] = s
+        m = 1 + torch.rand(x.shape[:-1], generator=g, device=dev)
+        x[..., 1] = (m if s < 0.5 else -7.5 * s * m).bfloat16()
+    Bn = len(scales)
+    part = tuple(x.expand(Bn, *x.shape[1:]).contiguous() for x in one)
+    params = B.make_params(hq, hkv, D, n, 1, THETA)
+    q = synth.normal_bf16((1, hq, D), 79, dev).expand(Bn, hq, D).contiguous()
+    pos = torch.tensor([seg * (i + 1) - 1 for i in range(Bn)], device=dev)
+    out, lse, st = _decode(params, B.make_cache_q4(part, None, Bn), q, pos, dev)
+    assert st.item() == 0
+    host = _part(part)
+
+    def rows_of(b):
+        r = seg * (b + 1)
+        (k, _, sk), (v, u, sv) = (_values(tuple(a[b, :, :r] for a in host), i) for i in (0, 1))
+        return tuple(x.swapaxes(0, 1).reshape(r, hkv, *t) for x, t in (
+            (k, (128,)), (v, (128,)), (sk, (2, 1)), (u, (2, 64)), (sv, (2, 1))))
+    _check_decode(params, q, out, lse, rows_of, ("scales", back))
+
+
+@pytest.mark.parametrize("value", [0.0, -1.0, 2.0 ** 29, 2.0 ** -40])
+def test_decode_constant_values(cuda_device, value):
+    """Every V row is one constant: so is the output (to its rounding and 2^-15 of the sums')."""
+    dev, hkv, hq, n = cuda_device, 1, 8, 5000
+    part = _random_store(1, hkv, n, 80, dev)
+    rec = part[2].view(1, hkv, n, 4, 2)
+    rec[..., 2:, 0], rec[..., 2:, 1] = 0.0, value
+    params = B.make_params(hq, hkv, D, n, 1, THETA)
+    q = synth.normal_bf16((1, hq, D), 81, dev)
+    out, _, _ = _decode(params, B.make_cache_q4(part, None, 1), q,
+                        torch.tensor([n - 1], device=dev), dev)
+    assert (np.abs(f64(out) - value) <= (2.0 ** -8 + 2.0 ** -15) * abs(value)).all()
+
+
 def _paged(dev, lp, w, positions, bad=None, hq=14, hkv=2):
     Bn = len(positions)
     params = B.make_params(hq, hkv, D, lp, w, THETA)
