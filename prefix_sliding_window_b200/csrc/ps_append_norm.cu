@@ -111,13 +111,8 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
       u[e] = fminf(u[e], 15.f);
     }
     if (ss > 0.f && ss < 1e-37f) {  // 1 / s overflows below 2^-128
-#pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        const float q = fminf(rintf(__fdiv_rn(x[c][e] - mm, ss)), 15.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i == e) u[i] = q;
-      }
+      for (int e = 0; e < 8; ++e) u[e] = fminf(rintf(__fdiv_rn(x[c][e] - mm, ss)), 15.f);
     }
     // halves of the word as sums of codes times 16^i, exact in fp32; 2^23 puts them into the
     // low mantissa bits
@@ -134,6 +129,9 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
 
 constexpr int kAhead = 4;  // items in flight a warp
 constexpr int kBlocksPerSm = 2;
+// Start positions of up to this many sequences are kept in shared memory (read from L2 twice a token
+// instead, 28 + 4 heads lose 1 us of the 8 that a warp takes for one).
+constexpr int kHeldBatch = kThreads;
 
 // Warps stride over the call's tokens; SPLIT of them share one (1 or 8).  A token's items are four
 // q heads each, then four rows each of its keys and values together (a K row and a V row cost
@@ -145,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
   __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
+  __shared__ int64_t s_pos0[SPLIT == 1 ? kHeldBatch : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
@@ -154,6 +153,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const int o1 = row * kHeadDim + 8 * p.c1, d2 = 8 * (p.c2 - p.c1);
   pdl_wait();
   pdl_trigger();
+
+  const int64_t* pos0 = a.pos0;
+  if (SPLIT == 1 && a.batch <= kHeldBatch) {
+    if (threadIdx.x < a.batch) s_pos0[threadIdx.x] = pos0[threadIdx.x];
+    __syncthreads();
+    pos0 = s_pos0;
+  }
 
   const int64_t end = items.any() ? a.batch * a.T : 0;
   // a token's sequence and place in it move on without divisions
@@ -168,21 +174,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     g.t += step_t;
     if (g.t >= a.T) g.t -= a.T, ++g.b;
   };
-  // where a token's rows go; `writes`: they go anywhere (a newer token of the call may own the
-  // ring slot)
+  // what a token's position says: the status bit where the store has no place for it; `kept`: its
+  // rows go to the store (a newer token of the call may own the ring slot)
   struct Token {
     int64_t pos;
-    StoreRow row;
-    bool writes;
+    int32_t flag;
+    bool kept;
   };
   auto token = [&](const Place& g) {
-    const int64_t p0 = a.pos0[g.b];
+    const int64_t p0 = pos0[g.b];
+    const StoreArgs& st = a.store;
     Token t;
     t.pos = p0 + g.t;
-    t.row = store_row(a.store, a.hkv, g.b, t.pos);
-    const bool stale =
-        !a.store.linear && t.pos >= a.store.lp && t.pos <= p0 + a.T - 1 - a.store.w;
-    t.writes = !t.row.flag && !stale;
+    t.flag = 0;
+    if (bad_rope_position(t.pos)) t.flag = rope_position_flag(t.pos);
+    else if (st.linear ? t.pos >= st.lp : t.pos < st.lp && !st.k[0]) t.flag = PS_DEV_POS_RANGE;
+    const bool stale = !st.linear && t.pos >= st.lp && t.pos <= p0 + a.T - 1 - st.w;
+    t.kept = !t.flag && !stale;
     return t;
   };
   Segment at = items.first(gw / SPLIT), far = at;
@@ -190,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   at_place.b = at.tok / a.T;
   at_place.t = static_cast<int32_t>(at.tok - at_place.b * a.T);
   far_place = at_place;
-  // moves `far` past the K and V segments of tokens that write none
+  // moves `far` past the K and V segments of tokens that keep none
   auto settle_far = [&]() {
-    while (far.tok < end && far.is_k && !token(far_place).writes) {
+    while (far.tok < end && far.is_k && !token(far_place).kept) {
       far = items.first(far.tok + items.step);
       next_place(far_place);
     }
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   };
   open();
   const uint4* ring_of = s_ring + warp * (kAhead + 1) * 2 * 32 + lane;
-  const uint32_t ring = smem_u32(ring_of);
+  const uint32_t ring_at = smem_u32(ring_of);
   constexpr uint32_t kItem = 2 * 32 * sizeof(uint4), kRing = (kAhead + 1) * kItem;
   uint32_t in = 0;
   auto load = [&]() {
@@ -217,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                          : a.v + far.tok * a.v_stride + (r - a.hkv) * kHeadDim;
         from += 8 * p.c1;
       }
-      copy16_if(ring + in, from, there);
-      copy16_if(ring + in + kItem / 2, from + d2, there);
+      copy16_if(ring_at + in, from, there);
+      copy16_if(ring_at + in + kItem / 2, from + d2, there);
       in = in == kRing - kItem ? 0 : in + kItem;
       src += items.kStride;
       const int64_t was = far.tok;
@@ -237,8 +245,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
   RowCoef coef;
   int64_t tok = -1;  // whose angles are in shared memory
-  bool fresh = true, skip = false, writes = false;
-  StoreRow place{0, 0, 0, 0};
+  bool fresh = true, skip = false, kept = false, writes = false;
+  int64_t store_at = 0, stride = 0;  // the token's row of head 0, rows from a head to the next
+  int32_t ring = 0, block = 0;
   __nv_bfloat16* dst = nullptr;
   uint32_t out = 0;
   while (at.tok < end) {
@@ -248,20 +257,38 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (at.tok != tok) {
         tok = at.tok;
         const Token t = token(at_place);
-        if (t.row.flag && a.status && lane == 0) atomicOr(a.status, t.row.flag);
-        // a token the store has no place for is skipped, its queries become zeros; a bad table
-        // entry only loses the row
+        if (t.flag && a.status && lane == 0) atomicOr(a.status, t.flag);
+        // a token the store has no place for is skipped, its queries become zeros
         const bool bad = bad_rope_position(t.pos);
-        skip = bad || (t.row.flag && !a.store.table);
-        place = t.row;
-        writes = t.writes;
-        if (!kv || writes)
-          rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+        skip = t.flag != 0;
+        kept = t.kept;
+        if (kept) {
+          const StoreArgs& st = a.store;
+          ring = t.pos >= st.lp;
+          store_at = ring ? mod_nonneg(t.pos - st.lp, st.w) : t.pos;
+          if (st.table)  // (looked at when the keys' turn comes)
+            block = st.table[at_place.b * st.table_stride + (ring ? st.pre_blocks : 0) +
+                             store_at / 64];
+        }
+        if (!kv || kept) rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
       }
-      if (kv && !writes) {  // on to the next token
+      if (kv && !kept) {  // on to the next token
         at = items.first(tok + items.step);
         next_place(at_place);
         continue;
+      }
+      if (kv) {
+        const StoreArgs& st = a.store;
+        writes = true;
+        stride = st.table ? 64 : ring ? st.w : st.lp;
+        if (st.table) {  // a bad entry only loses the row
+          writes = block >= 0 && block < st.n_blocks;
+          if (!writes && a.status && lane == 0) atomicOr(a.status, PS_DEV_POS_RANGE);
+          store_at = (int64_t)block * a.hkv * 64 + store_at % 64;
+          ring = 0;  // one pool holds both
+        } else {
+          store_at += at_place.b * a.hkv * stride;
+        }
       }
       row_coef<INTER>(p, kv && norm, s_w + (kv ? kHeadDim : 0), s_cos[warp], s_sin[warp], coef);
       if (!kv) dst = a.q_out + (tok * a.hq + items.q0 * 4) * kHeadDim + o1;
@@ -273,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     float u[8], v[8];
     unpack_pairs<INTER>(r1, r2, u, v);
     uint4 y1, y2;
-    const bool live = row < at.rows;
+    const bool live = row < at.rows && (!kv || writes);
     if (!kv) {
       norm_and_turn(p, norm, false, coef, a.norm.eps, u, v);
       pack_pairs<INTER>(u, v, y1, y2);
@@ -289,11 +316,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const int r = 2 * a.hkv - at.rows + row;
       const bool is_v = r >= a.hkv;
       if (is_v) y1 = r1, y2 = r2;  // values as they are
-      const int64_t to = place.unit + (is_v ? r - a.hkv : r) * place.stride;
-      uint8_t* base = is_v ? a.store.v[place.ring] : a.store.k[place.ring];
+      const int64_t to = store_at + (is_v ? r - a.hkv : r) * stride;
+      uint8_t* base = is_v ? a.store.v[ring] : a.store.k[ring];
       if (Q4) {
         quantise_row(p, y1, y2, live, lane & 7, base + to * kQ4RowBytes,
-                     a.store.s[place.ring] + to * kQ4RecordBytes + (is_v ? 8 : 0));
+                     a.store.s[ring] + to * kQ4RecordBytes + (is_v ? 8 : 0));
       } else if (live) {
         __nv_bfloat16* to_row = reinterpret_cast<__nv_bfloat16*>(base) + to * kHeadDim + 8 * p.c1;
         *reinterpret_cast<uint4*>(to_row) = y1;
