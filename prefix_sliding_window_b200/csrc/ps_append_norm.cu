@@ -3,8 +3,9 @@
 //
 // One pass: a token's packed q, k and v heads are read once; keys are normalised, rotated at the
 // token's position and written to their prefix row or ring slot, values go straight there, queries
-// to q_out.  Bound by HBM for long prompts (one read and one write a row) and by latency for a
-// decode step's single tokens.  Of tokens that share a ring slot only the newest of the call is
+// to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half of
+// them kept: 107 us, 78 % of a copy's rate; into 4 bits 122 us) and by latency for a decode step's
+// single tokens.  Of tokens that share a ring slot only the newest of the call is
 // written, so the result does not depend on which block runs first.
 //
 // A warp keeps a token's angles and weights in registers over all of its heads, as in the pass
@@ -23,70 +24,50 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Least and greatest of two or of a row's eight lanes; a NaN stays one.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Least and greatest of two bf16 pairs; a NaN stays one.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float row_min(float v) {
-  v = min_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = min_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  return min_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
+// A chunk's least value and its greatest one's negative, a bf16 each: the least of two such words is
+// both again.
+__device__ __forceinline__ uint32_t span_word(const uint4& w) {
+  const uint32_t lo = min2_nan(min2_nan(w.x, w.y), min2_nan(w.z, w.w));
+  const uint32_t hi = max2_nan(max2_nan(w.x, w.y), max2_nan(w.z, w.w));
+  return min2_nan(__byte_perm(lo, hi, 0x5410) ^ 0x80000000u,
+                  __byte_perm(lo, hi, 0x7632) ^ 0x80000000u);
 }
-__device__ __forceinline__ float row_max(float v) {
-  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  return max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
-}
-
-// The same of three.
-__device__ __forceinline__ float min3_nan(float a, float b, float c) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
+__device__ __forceinline__ uint32_t row_span(uint32_t v) {
+  v = min2_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = min2_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  return min2_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
 }
 
 // Quantises a row held by eight lanes (chunks p.c1, p.c2 of a lane, bf16) and writes it: payload
 // words at `pay`, (s, m) of both groups at `rec` (8 bytes).  All lanes take part; only `live` ones
 // write.
 //
-// A code is (x - m) / s rounded to nearest even, by a product with 1 / s (within 2e-6 of the
+// A code is (x - m) / s rounded to nearest even, by a product with 1 / s (within 1e-5 of the
 // quotient) and the remainder r = (x - m) - u s, which one fma gives exactly: beyond s / 2, or at
 // s / 2 with u odd, the code is one further on.  (On the bf16 grid such ties are common: dividing
 // where a product was near one ran for nearly every warp.)
 __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1, const uint4& r2,
                                              bool live, int lane8, uint8_t* pay, uint8_t* rec) {
-  float x[2][8], lo[2], hi[2];
-  const uint32_t w[2][4] = {{r1.x, r1.y, r1.z, r1.w}, {r2.x, r2.y, r2.z, r2.w}};
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[c][2 * i] = __uint_as_float(w[c][i] << 16);
-      x[c][2 * i + 1] = __uint_as_float(w[c][i] & 0xffff0000u);
-    }
-    const float* v = x[c];
-    lo[c] = min_nan(min3_nan(min3_nan(v[0], v[1], v[2]), v[3], v[4]), min3_nan(v[5], v[6], v[7]));
-    hi[c] = max_nan(max3_nan(max3_nan(v[0], v[1], v[2]), v[3], v[4]), max3_nan(v[5], v[6], v[7]));
-  }
   const int g1 = p.c1 >> 3, g2 = p.c2 >> 3;
+  const uint32_t span1 = span_word(r1), span2 = span_word(r2);
   float m[2], s[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    m[g] = row_min(min_nan(g1 == g ? lo[0] : INFINITY, g2 == g ? lo[1] : INFINITY));
-    const float most =
-        row_max(max_nan(g1 == g ? hi[0] : -INFINITY, g2 == g ? hi[1] : -INFINITY));
+    constexpr uint32_t kNone = 0x7f807f80u;  // infinities
+    const uint32_t span = row_span(min2_nan(g1 == g ? span1 : kNone, g2 == g ? span2 : kNone));
+    m[g] = __uint_as_float(span << 16);
+    const float most = -__uint_as_float(span & 0xffff0000u);
     s[g] = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(most - m[g], 15.f)));
     if (!(s[g] < INFINITY)) m[g] = s[g] = __uint_as_float(0x7fc00000u);
   }
@@ -95,24 +76,30 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
   for (int c = 0; c < 2; ++c) {
     const int chunk = c ? p.c2 : p.c1;
     const int g = chunk >> 3, b = chunk & 7;
+    const uint4& rw = c ? r2 : r1;
+    const uint32_t w[4] = {rw.x, rw.y, rw.z, rw.w};
     const float mm = g ? m[1] : m[0], ss = g ? s[1] : s[0];
-    const float inv = __fdiv_rn(1.f, ss);
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ss));
     const uint32_t half = __float_as_uint(0.5f * ss);
     float u[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = __fsub_rn(x[c][e], mm);
-      const float t = fmaf(d, inv, round);
-      u[e] = t - round;
-      const float r = fmaf(-u[e], ss, d);
+    for (int i = 0; i < 8; ++i) {  // (as packed operations, two values each, it took 6 % longer)
+      const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+      const float d = __fsub_rn(x, mm), t = fmaf(d, inv, round);
+      u[i] = t - round;
+      const float r = fmaf(-u[i], ss, d);
       // an odd code leaves at the border already: its bound is the float below s / 2
       const float bound = __uint_as_float(half - (__float_as_uint(t) & 1u));
-      if (fabsf(r) > bound) u[e] += copysignf(1.f, r);
-      u[e] = fminf(u[e], 15.f);
+      if (fabsf(r) > bound) u[i] += copysignf(1.f, r);
+      u[i] = fminf(u[i], 15.f);
     }
     if (ss > 0.f && ss < 1e-37f) {  // 1 / s overflows below 2^-128
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = fminf(rintf(__fdiv_rn(x[c][e] - mm, ss)), 15.f);
+      for (int i = 0; i < 8; ++i) {
+        const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        u[i] = fminf(rintf(__fdiv_rn(x - mm, ss)), 15.f);
+      }
     }
     // halves of the word as sums of codes times 16^i, exact in fp32; 2^23 puts them into the
     // low mantissa bits
@@ -129,8 +116,8 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
 
 constexpr int kAhead = 4;  // items in flight a warp
 constexpr int kBlocksPerSm = 2;
-// Start positions of up to this many sequences are kept in shared memory (read from L2 twice a token
-// instead, 28 + 4 heads lose 1 us of the 8 that a warp takes for one).
+// Start positions of up to this many sequences are kept in shared memory (every warp reads its
+// tokens' twice; from L2 they cost 1 us of 114 at 4 x 8192 tokens).
 constexpr int kHeldBatch = kThreads;
 
 // Warps stride over the call's tokens; SPLIT of them share one (1 or 8).  A token's items are four
@@ -174,23 +161,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     g.t += step_t;
     if (g.t >= a.T) g.t -= a.T, ++g.b;
   };
-  // what a token's position says: the status bit where the store has no place for it; `kept`: its
-  // rows go to the store (a newer token of the call may own the ring slot)
+  // what a token's position says (`pos` where it is not `bad`); `none`: the store has no place for
+  // it; `kept`: its rows go to the store (a newer token of the call may own the ring slot)
   struct Token {
-    int64_t pos;
-    int32_t flag;
-    bool kept;
+    int32_t pos;
+    bool bad, none, kept;
   };
+  const int32_t fresh_from = a.store.linear ? 0 : max(a.T - a.store.w, 0);
+  const bool no_prefix = !a.store.linear && !a.store.k[0];
   auto token = [&](const Place& g) {
-    const int64_t p0 = pos0[g.b];
-    const StoreArgs& st = a.store;
+    const uint64_t p = static_cast<uint64_t>(pos0[g.b] + g.t);
     Token t;
-    t.pos = p0 + g.t;
-    t.flag = 0;
-    if (bad_rope_position(t.pos)) t.flag = rope_position_flag(t.pos);
-    else if (st.linear ? t.pos >= st.lp : t.pos < st.lp && !st.k[0]) t.flag = PS_DEV_POS_RANGE;
-    const bool stale = !st.linear && t.pos >= st.lp && t.pos <= p0 + a.T - 1 - st.w;
-    t.kept = !t.flag && !stale;
+    t.pos = static_cast<int32_t>(p);
+    t.bad = p >= (1ull << 31);
+    const bool prefix = t.pos < a.store.lp;
+    t.none = t.bad | (a.store.linear ? !prefix : prefix & no_prefix);
+    t.kept = !t.none & (prefix | (g.t >= fresh_from));
     return t;
   };
   Segment at = items.first(gw / SPLIT), far = at;
@@ -257,20 +243,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (at.tok != tok) {
         tok = at.tok;
         const Token t = token(at_place);
-        if (t.flag && a.status && lane == 0) atomicOr(a.status, t.flag);
+        if (t.none && a.status && lane == 0)
+          atomicOr(a.status, t.bad && pos0[at_place.b] + at_place.t < 0 ? PS_DEV_BAD_POS
+                                                                         : PS_DEV_POS_RANGE);
         // a token the store has no place for is skipped, its queries become zeros
-        const bool bad = bad_rope_position(t.pos);
-        skip = t.flag != 0;
+        skip = t.none;
         kept = t.kept;
         if (kept) {
           const StoreArgs& st = a.store;
           ring = t.pos >= st.lp;
-          store_at = ring ? mod_nonneg(t.pos - st.lp, st.w) : t.pos;
+          const uint32_t slot = static_cast<uint32_t>(t.pos) - static_cast<uint32_t>(st.lp);
+          store_at = ring ? slot % static_cast<uint32_t>(st.w) : t.pos;
           if (st.table)  // (looked at when the keys' turn comes)
             block = st.table[at_place.b * st.table_stride + (ring ? st.pre_blocks : 0) +
                              store_at / 64];
         }
-        if (!kv || kept) rope_angles(a.rope, bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+        if (!kv || kept) rope_angles(a.rope, t.bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
       }
       if (kv && !kept) {  // on to the next token
         at = items.first(tok + items.step);
@@ -297,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     copies_wait<kAhead>();
     const uint4 r1 = ring_of[out / sizeof(uint4)], r2 = ring_of[out / sizeof(uint4) + 32];
     out = out == kRing - kItem ? 0 : out + kItem;
-    float u[8], v[8];
+    uint64_t u[4], v[4];
     unpack_pairs<INTER>(r1, r2, u, v);
     uint4 y1, y2;
     const bool live = row < at.rows && (!kv || writes);

@@ -9,8 +9,8 @@
 // prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
 // 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
 //
-// At 4 x 8192 tokens of 28 + 4 heads the forward takes 92 us (5.8 TB/s, 90 % of a copy's rate), the
-// backward 137 us (91 %).
+// At 4 x 8192 tokens of 28 + 4 heads the forward takes 88 us (6.1 TB/s, 94 % of a copy's rate), the
+// backward 134 us (93 %).  Three blocks of 80 registers an SM: 97 and more.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     }
     load();
     copies_wait<kAhead>();
-    float u[8], v[8];
+    uint64_t u[4], v[4];
     const uint4* r = &s_ring[warp][0][0][lane] + out / sizeof(uint4);
     unpack_pairs<INTER>(r[0], r[32], u, v);
     out = out == kRing - kItem ? 0 : out + kItem;
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   for (int i = 0; i < 8; ++i) s_dwk[warp][i][lane] = 0;
   __syncthreads();
 
-  float dwu[8], dwv[8];  // query weight's gradient, this lane's pairs
-  float wu[8], wv[8], c[8], s[8], ns[8];
+  uint64_t dwu[4], dwv[4];  // query weight's gradient, this lane's pairs
+  uint64_t wu[4], wv[4], c[4], s[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwu[i] = dwv[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dwu[i] = dwv[i] = 0;
   int64_t tok = -1;
   bool bad = false, fresh = true;
   __nv_bfloat16* dst = nullptr;
@@ -188,8 +188,6 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
         if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
         rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
         lane_angles(p, s_cos[warp], s_sin[warp], c, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ns[i] = -s[i];
       }
       lane_weights<INTER>(s_w + (is_k ? kHeadDim : 0), p, wu, wv);
       dst = is_k ? a.dk + tok * a.dk_stride + items.k0 * 4 * kHeadDim + o1
@@ -202,17 +200,17 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
     const bool live = row < at.rows;
     uint4 y1 = make_uint4(0, 0, 0, 0), y2 = y1;
     if (!bad) {
-      float gu[8], gv[8];
+      uint64_t gu[4], gv[4];
       unpack_pairs<INTER>(r[0], r[32], gu, gv);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i < 2 ? p.rot1 : p.rot2) {
-          const uint64_t x = pair_of(gu, i), y = pair_of(gv, i);
-          set_pair(gu, i, ffma2(y, pair_of(s, i), fmul2(x, pair_of(c, i))));
-          set_pair(gv, i, ffma2(x, pair_of(ns, i), fmul2(y, pair_of(c, i))));
+          const uint64_t x = gu[i], y = gv[i];
+          gu[i] = ffma2(y, s[i], fmul2(x, c[i]));
+          gv[i] = ffma2(fmul2(x, s[i]), pack_f32x2(-1.f, -1.f), fmul2(y, c[i]));
         }
       if (norm) {
-        float nu[8], nv[8];
+        uint64_t nu[4], nv[4];
         unpack_pairs<INTER>(r[64], r[96], nu, nv);
         float rstd = row_rstd(nu, nv, a.norm.eps);
         if (!live) rstd = 0.f;  // (eps may be 0)
@@ -220,29 +218,29 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
         uint64_t dot = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint64_t x = fmul2(pair_of(nu, i), r2), y = fmul2(pair_of(nv, i), r2);
-          const uint64_t gx = pair_of(gu, i), gy = pair_of(gv, i);
-          set_pair(nu, i, x);
-          set_pair(nv, i, y);
+          const uint64_t x = fmul2(nu[i], r2), y = fmul2(nv[i], r2);
+          const uint64_t gx = gu[i], gy = gv[i];
+          nu[i] = x;
+          nv[i] = y;
           if (is_k) {
             s_dwk[warp][i][lane] = ffma2(gx, x, s_dwk[warp][i][lane]);
             s_dwk[warp][4 + i][lane] = ffma2(gy, y, s_dwk[warp][4 + i][lane]);
           } else {
-            set_pair(dwu, i, ffma2(gx, x, pair_of(dwu, i)));
-            set_pair(dwv, i, ffma2(gy, y, pair_of(dwv, i)));
+            dwu[i] = ffma2(gx, x, dwu[i]);
+            dwv[i] = ffma2(gy, y, dwv[i]);
           }
-          const uint64_t hx = fmul2(gx, pair_of(wu, i)), hy = fmul2(gy, pair_of(wv, i));
+          const uint64_t hx = fmul2(gx, wu[i]), hy = fmul2(gy, wv[i]);
           dot = ffma2(hy, y, ffma2(hx, x, dot));
-          set_pair(gu, i, hx);
-          set_pair(gv, i, hy);
+          gu[i] = hx;
+          gv[i] = hy;
         }
         const float2 d = unpack_f32x2(dot);
         const float mean = row_sum(d.x + d.y) * (-1.f / kHeadDim);
         const uint64_t m2 = pack_f32x2(mean, mean);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          set_pair(gu, i, fmul2(r2, ffma2(pair_of(nu, i), m2, pair_of(gu, i))));
-          set_pair(gv, i, fmul2(r2, ffma2(pair_of(nv, i), m2, pair_of(gv, i))));
+          gu[i] = fmul2(r2, ffma2(nu[i], m2, gu[i]));
+          gv[i] = fmul2(r2, ffma2(nv[i], m2, gv[i]));
         }
       }
       pack_pairs<INTER>(gu, gv, y1, y2);
@@ -260,7 +258,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   for (int i = 0; i < 8; ++i) {
     const float2 ku = unpack_f32x2(s_dwk[warp][i >> 1][lane]);
     const float2 kv = unpack_f32x2(s_dwk[warp][4 + (i >> 1)][lane]);
-    float x[4] = {dwu[i], dwv[i], (i & 1) ? ku.y : ku.x, (i & 1) ? kv.y : kv.x};
+    const float2 qu = unpack_f32x2(dwu[i >> 1]), qv = unpack_f32x2(dwv[i >> 1]);
+    float x[4] = {(i & 1) ? qu.y : qu.x, (i & 1) ? qv.y : qv.x, (i & 1) ? ku.y : ku.x,
+                  (i & 1) ? kv.y : kv.x};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       x[j] += __shfl_xor_sync(0xffffffffu, x[j], 8);

@@ -61,37 +61,45 @@ __device__ __forceinline__ int32_t rope_position_flag(int64_t p) {
   return p < 0 ? PS_DEV_BAD_POS : PS_DEV_POS_RANGE;
 }
 
-// A lane's chunks as pairs and back; INTER: the interleaved layout (a template parameter: as a
-// flag it costs a select an element).
+// A lane's chunks as its eight (u, v) and back, two neighbouring floats to an operand of the packed
+// fp32 instructions, which do two lanes of the work in one issue.  INTER: the interleaved layout (a
+// template parameter: as a flag it costs a select an element).
+__device__ __forceinline__ uint64_t both(uint32_t lo, uint32_t hi) {
+  return pack_f32x2(__uint_as_float(lo), __uint_as_float(hi));
+}
 template <bool INTER>
-__device__ __forceinline__ void unpack_pairs(const uint4& c1, const uint4& c2, float (&u)[8],
-                                             float (&v)[8]) {
+__device__ __forceinline__ void unpack_pairs(const uint4& c1, const uint4& c2, uint64_t (&u)[4],
+                                             uint64_t (&v)[4]) {
   const uint32_t a[4] = {c1.x, c1.y, c1.z, c1.w}, b[4] = {c2.x, c2.y, c2.z, c2.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float al = __uint_as_float(a[i] << 16), ah = __uint_as_float(a[i] & 0xffff0000u);
-    const float bl = __uint_as_float(b[i] << 16), bh = __uint_as_float(b[i] & 0xffff0000u);
     if (INTER) {
-      u[i] = al, v[i] = ah, u[4 + i] = bl, v[4 + i] = bh;
+      const uint32_t x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+      u[i] = both(x << 16, y << 16);
+      v[i] = both(x & 0xffff0000u, y & 0xffff0000u);
     } else {
-      u[2 * i] = al, u[2 * i + 1] = ah, v[2 * i] = bl, v[2 * i + 1] = bh;
+      u[i] = both(a[i] << 16, a[i] & 0xffff0000u);
+      v[i] = both(b[i] << 16, b[i] & 0xffff0000u);
     }
   }
 }
 template <bool INTER>
-__device__ __forceinline__ void pack_pairs(const float (&u)[8], const float (&v)[8], uint4& c1,
-                                           uint4& c2) {
-  if (INTER) {
-    c1 = make_uint4(cvt_bf16x2(u[0], v[0]), cvt_bf16x2(u[1], v[1]), cvt_bf16x2(u[2], v[2]),
-                    cvt_bf16x2(u[3], v[3]));
-    c2 = make_uint4(cvt_bf16x2(u[4], v[4]), cvt_bf16x2(u[5], v[5]), cvt_bf16x2(u[6], v[6]),
-                    cvt_bf16x2(u[7], v[7]));
-  } else {
-    c1 = make_uint4(cvt_bf16x2(u[0], u[1]), cvt_bf16x2(u[2], u[3]), cvt_bf16x2(u[4], u[5]),
-                    cvt_bf16x2(u[6], u[7]));
-    c2 = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
-                    cvt_bf16x2(v[6], v[7]));
+__device__ __forceinline__ void pack_pairs(const uint64_t (&u)[4], const uint64_t (&v)[4],
+                                           uint4& c1, uint4& c2) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack_f32x2(u[i]), y = unpack_f32x2(v[i]);
+    if (INTER) {
+      (i < 2 ? a[2 * i] : b[2 * i - 4]) = cvt_bf16x2(x.x, y.x);
+      (i < 2 ? a[2 * i + 1] : b[2 * i - 3]) = cvt_bf16x2(x.y, y.y);
+    } else {
+      a[i] = cvt_bf16x2(x.x, x.y);
+      b[i] = cvt_bf16x2(y.x, y.y);
+    }
   }
+  c1 = make_uint4(a[0], a[1], a[2], a[3]);
+  c2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // cos and sin of p * inv_f: reduced to [-pi/4, pi/4] in float64 (pi/2 in two parts; the first
@@ -178,17 +186,6 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Two neighbouring floats as one operand of the packed fp32 instructions, which do two lanes of
-// the work in one issue.
-__device__ __forceinline__ uint64_t pair_of(const float (&x)[8], int i) {
-  return pack_f32x2(x[2 * i], x[2 * i + 1]);
-}
-__device__ __forceinline__ void set_pair(float (&x)[8], int i, uint64_t v) {
-  const float2 f = unpack_f32x2(v);
-  x[2 * i] = f.x;
-  x[2 * i + 1] = f.y;
-}
-
 // A product that is rounded by itself, whatever is done with it.
 __device__ __forceinline__ uint64_t fmul2_rn(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -197,12 +194,13 @@ __device__ __forceinline__ uint64_t fmul2_rn(uint64_t a, uint64_t b) {
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a row held by eight lanes, fp32.
-__device__ __forceinline__ float row_rstd(const float (&u)[8], const float (&v)[8], float eps) {
+__device__ __forceinline__ float row_rstd(const uint64_t (&u)[4], const uint64_t (&v)[4],
+                                          float eps) {
   uint64_t s = 0, t = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s = ffma2(pair_of(u, i), pair_of(u, i), s);
-    t = ffma2(pair_of(v, i), pair_of(v, i), t);
+    s = ffma2(u[i], u[i], s);
+    t = ffma2(v[i], v[i], t);
   }
   const float2 x = unpack_f32x2(fadd2(s, t));
   return rsqrtf(row_sum(x.x + x.y) * (1.f / kHeadDim) + eps);
@@ -222,40 +220,41 @@ __device__ __forceinline__ void load_norm_weights(const NormArgs& n, float* s_w)
 
 // A lane's weights as pairs.
 template <bool INTER>
-__device__ __forceinline__ void lane_weights(const float* w, const RopeLane& p, float (&wu)[8],
-                                             float (&wv)[8]) {
-  float x[8], y[8];
+__device__ __forceinline__ void lane_weights(const float* w, const RopeLane& p, uint64_t (&wu)[4],
+                                             uint64_t (&wv)[4]) {
+  uint64_t x[8];  // both chunks
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 a = *reinterpret_cast<const float4*>(w + 8 * p.c1 + 4 * i);
-    const float4 b = *reinterpret_cast<const float4*>(w + 8 * p.c2 + 4 * i);
-    x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = a.z, x[4 * i + 3] = a.w;
-    y[4 * i] = b.x, y[4 * i + 1] = b.y, y[4 * i + 2] = b.z, y[4 * i + 3] = b.w;
+  for (int i = 0; i < 4; ++i) {
+    const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(
+        w + 8 * (i < 2 ? p.c1 : p.c2) + 4 * (i & 1));
+    x[2 * i] = y.x, x[2 * i + 1] = y.y;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (INTER) {
-      wu[i] = x[2 * i], wv[i] = x[2 * i + 1], wu[4 + i] = y[2 * i], wv[4 + i] = y[2 * i + 1];
+      const float2 a = unpack_f32x2(x[2 * i]), b = unpack_f32x2(x[2 * i + 1]);
+      wu[i] = pack_f32x2(a.x, b.x);
+      wv[i] = pack_f32x2(a.y, b.y);
     } else {
-      wu[2 * i] = x[2 * i], wu[2 * i + 1] = x[2 * i + 1];
-      wv[2 * i] = y[2 * i], wv[2 * i + 1] = y[2 * i + 1];
+      wu[i] = x[i];
+      wv[i] = x[4 + i];
     }
   }
 }
 
 // A lane's cosines and sines (1 and 0 where a pair is not rotated).
 __device__ __forceinline__ void lane_angles(const RopeLane& p, const float* cos, const float* sin,
-                                            float (&c)[8], float (&s)[8]) {
+                                            uint64_t (&c)[4], uint64_t (&s)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bool rot = i ? p.rot2 : p.rot1;
-    float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (rot) {
-      x = *reinterpret_cast<const float4*>(cos + (i ? p.a2 : p.a1));
-      y = *reinterpret_cast<const float4*>(sin + (i ? p.a2 : p.a1));
+    const uint64_t one = pack_f32x2(1.f, 1.f);
+    ulonglong2 x = make_ulonglong2(one, one), y = make_ulonglong2(0, 0);
+    if (i ? p.rot2 : p.rot1) {
+      x = *reinterpret_cast<const ulonglong2*>(cos + (i ? p.a2 : p.a1));
+      y = *reinterpret_cast<const ulonglong2*>(sin + (i ? p.a2 : p.a1));
     }
-    c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-    s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+    c[2 * i] = x.x, c[2 * i + 1] = x.y;
+    s[2 * i] = y.x, s[2 * i + 1] = y.y;
   }
 }
 
@@ -263,7 +262,7 @@ __device__ __forceinline__ void lane_angles(const RopeLane& p, const float* cos,
 // norm) are in the angles, and b is negative.  Of normalised keys: a and c are the weights of u and
 // v, b and d cosines and sines.
 struct RowCoef {
-  float a[8], b[8], c[8], d[8];
+  uint64_t a[4], b[4], c[4], d[4];
 };
 template <bool INTER>
 __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const float* w,
@@ -273,18 +272,16 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const floa
     lane_weights<INTER>(w, p, k.a, k.c);
     return;
   }
-  float c[8], s[8], wu[8], wv[8];
+  uint64_t c[4], s[4], wu[4], wv[4];
   lane_angles(p, cos, sin, c, s);
   lane_weights<INTER>(w, p, wu, wv);
   const uint64_t minus = pack_f32x2(-1.f, -1.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint64_t cc = pair_of(c, i), ss = pair_of(s, i);
-    const uint64_t u = pair_of(wu, i), v = pair_of(wv, i);
-    set_pair(k.a, i, fmul2(u, cc));
-    set_pair(k.b, i, fmul2(fmul2(v, ss), minus));
-    set_pair(k.c, i, fmul2(v, cc));
-    set_pair(k.d, i, fmul2(u, ss));
+    k.a[i] = fmul2(wu[i], c[i]);
+    k.b[i] = fmul2(fmul2(wv[i], s[i]), minus);
+    k.c[i] = fmul2(wv[i], c[i]);
+    k.d[i] = fmul2(wu[i], s[i]);
   }
 }
 
@@ -293,8 +290,8 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const floa
 // plain evaluation does: a 4-bit store turns a last bit that differs into a whole code now and then,
 // and a token has few key heads.
 __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool key,
-                                              const RowCoef& k, float eps, float (&u)[8],
-                                              float (&v)[8]) {
+                                              const RowCoef& k, float eps, uint64_t (&u)[4],
+                                              uint64_t (&v)[4]) {
   if (norm) {
     const float rstd = row_rstd(u, v, eps);
     const uint64_t r2 = pack_f32x2(rstd, rstd);
@@ -302,37 +299,37 @@ __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool
       const uint64_t minus = pack_f32x2(-1.f, -1.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint64_t x = fmul2_rn(fmul2_rn(pair_of(u, i), r2), pair_of(k.a, i));
-        uint64_t y = fmul2_rn(fmul2_rn(pair_of(v, i), r2), pair_of(k.c, i));
+        uint64_t x = fmul2_rn(fmul2_rn(u[i], r2), k.a[i]);
+        uint64_t y = fmul2_rn(fmul2_rn(v[i], r2), k.c[i]);
         if (i < 2 ? p.rot1 : p.rot2) {
-          const uint64_t c = pair_of(k.b, i), s = pair_of(k.d, i);
-          const uint64_t xs = fmul2_rn(x, s), ys = fmul2_rn(y, s);
-          x = ffma2(ys, minus, fmul2_rn(x, c));
-          y = fadd2(fmul2_rn(y, c), xs);
+          const uint64_t xs = fmul2_rn(x, k.d[i]), ys = fmul2_rn(y, k.d[i]);
+          x = ffma2(ys, minus, fmul2_rn(x, k.b[i]));
+          y = fadd2(fmul2_rn(y, k.b[i]), xs);
         }
-        set_pair(u, i, x);
-        set_pair(v, i, y);
+        u[i] = x;
+        v[i] = y;
       }
       return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t uu = pair_of(u, i), vv = pair_of(v, i);
-      uint64_t x = fmul2(uu, pair_of(k.a, i)), y = fmul2(vv, pair_of(k.c, i));
+      uint64_t x = fmul2(u[i], k.a[i]), y = fmul2(v[i], k.c[i]);
       if (i < 2 ? p.rot1 : p.rot2) {  // (an infinity reaches its own pair only)
-        x = ffma2(vv, pair_of(k.b, i), x);
-        y = ffma2(uu, pair_of(k.d, i), y);
+        x = ffma2(v[i], k.b[i], x);
+        y = ffma2(u[i], k.d[i], y);
       }
-      set_pair(u, i, fmul2(x, r2));
-      set_pair(v, i, fmul2(y, r2));
+      u[i] = fmul2(x, r2);
+      v[i] = fmul2(y, r2);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < 4 ? p.rot1 : p.rot2) {
-        const float x = rope_lo(u[i], v[i], k.a[i], -k.b[i]);
-        v[i] = rope_hi(u[i], v[i], k.c[i], k.d[i]);
-        u[i] = x;
+    for (int i = 0; i < 4; ++i)
+      if (i < 2 ? p.rot1 : p.rot2) {
+        const float2 x = unpack_f32x2(u[i]), y = unpack_f32x2(v[i]);
+        const float2 a = unpack_f32x2(k.a[i]), b = unpack_f32x2(k.b[i]);
+        const float2 c = unpack_f32x2(k.c[i]), d = unpack_f32x2(k.d[i]);
+        u[i] = pack_f32x2(rope_lo(x.x, y.x, a.x, -b.x), rope_lo(x.y, y.y, a.y, -b.y));
+        v[i] = pack_f32x2(rope_hi(x.x, y.x, c.x, d.x), rope_hi(x.y, y.y, c.y, d.y));
       }
   }
 }
