@@ -513,6 +513,10 @@ def _heads(name: str, t, tokens: int, heads: int, device: int):
     """Rows of heads: [tokens, heads, 128] (or leading dims that flatten to tokens) with heads
     contiguous in a token.  Returns the address and the stride between tokens."""
     sh, st = t.shape, t.stride()
+    if len(sh) == 3 and st[2] == 1 and st[1] == 128 and sh[2] == 128 and sh[1] == heads and \
+            sh[0] == tokens > 1 and t.dtype is _torch_module.bfloat16 and \
+            t.get_device() == device:
+        return t.data_ptr(), st[0]  # the usual case, decided in few steps
     ok = (t.dtype is _torch().bfloat16 and t.get_device() == device and len(sh) >= 3
           and sh[-1] == 128 and sh[-2] == heads and st[-1] == 1 and (st[-2] == 128 or heads == 1))
     n, stride = 1, heads * 128
@@ -532,20 +536,27 @@ def _heads(name: str, t, tokens: int, heads: int, device: int):
 
 
 _torch_module = None
+_current_device = _current_stream = None  # (device index), (device index -> handle)
 
 
 def _torch():
-    global _torch_module
+    """torch, and the runtime's own calls for the current device and stream where torch offers
+    them: the public ones build objects, which takes longer than a launch."""
+    global _torch_module, _current_device, _current_stream
     if _torch_module is None:
         import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda _: _stream(None))
         _torch_module = torch
     return _torch_module
 
 
 def _device_of(pos, norm=None, cache=None) -> int:
     """The device index of a call: the current device, where everything it is given lives."""
+    if _torch_module is None:
+        _torch()
     dev = pos.get_device()
-    if dev < 0 or dev != _torch().cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"positions are on {pos.device}, the current device is "
                          f"cuda:{_torch().cuda.current_device()}")
     for what in (norm, cache):
@@ -555,12 +566,8 @@ def _device_of(pos, norm=None, cache=None) -> int:
 
 
 def _stream_on(stream, device: int):
-    """The stream's handle; None: the current stream of the device.  (Asked of the runtime by its
-    raw handle where torch offers that: building a Stream object takes longer than a launch.)"""
-    if stream is not None:
-        return _stream(stream)
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else _stream(None)
+    """The stream's handle; None: the current stream of the device."""
+    return _current_stream(device) if stream is None else _stream(stream)
 
 
 def _workspace(ws, device: int):
@@ -573,7 +580,7 @@ def _workspace(ws, device: int):
 
 
 def _status_ptr(t, device: int):
-    return None if t is None else _tensor("dev_status", t, _torch().int32, device, 1)
+    return None if t is None else _tensor("dev_status", t, _torch_module.int32, device, 1)
 
 
 def ps_qk_norm_rope(params: PsParams, rope: PsRope, norm, q, k, pos, q_out, k_out,
