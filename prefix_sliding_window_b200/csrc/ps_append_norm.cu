@@ -4,8 +4,8 @@
 // One pass: a token's packed q, k and v heads are read once; keys are normalised, rotated at the
 // token's position and written to their prefix row or ring slot, values go straight there, queries
 // to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half
-// of them kept: 107 us, 78 % of a copy's rate; into 4 bits 122 us) and by latency for a decode step's
-// single tokens.  Of tokens that share a ring slot only the newest of the call is written, so the
+// of them kept: 103 us, 81 % of a copy's rate; into 4 bits 120 us) and by latency for a decode
+// step's single tokens.  Of tokens that share a ring slot only the newest of the call is written, so the
 // result does not depend on which block runs first.
 //
 // A warp keeps a token's angles and weights in registers over all of its heads, as in the pass
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
   __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
+  __shared__ double s_freq[kHalfDim];
   __shared__ int64_t s_pos0[SPLIT == 1 ? kHeldBatch : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll 1
   for (int i = 0; i < kAhead; ++i) load();
   load_norm_weights(a.norm, s_w);
+  load_frequencies(a.rope, s_freq);
   __syncthreads();
 
   RowCoef coef;
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             block = st.table[at_place.b * st.table_stride + (ring ? st.pre_blocks : 0) +
                              store_at / 64];
         }
-        if (!kv || kept) rope_angles(a.rope, t.bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+        if (!kv || kept) rope_angles(a.rope, s_freq, t.bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
       }
       if (kv && !kept) {  // on to the next token
         at = items.first(tok + items.step);

@@ -9,8 +9,8 @@
 // prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
 // 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
 //
-// At 4 x 8192 tokens of 28 + 4 heads the forward takes 88 us (6.1 TB/s, 94 % of a copy's rate), the
-// backward 134 us (93 %).  Three blocks of 80 registers an SM: 97 and more.
+// At 4 x 8192 tokens of 28 + 4 heads the forward takes 89 us (6.0 TB/s, 93 % of a copy's rate), the
+// backward 132 us (95 %).  Three blocks of 80 registers an SM: 97 and more.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
   __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
   __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
+  __shared__ double s_freq[kHalfDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopeLane p = rope_lane<INTER>(a.rope, lane & 7);
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
@@ -65,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
 #pragma unroll 1
   for (int i = 0; i < kAhead; ++i) load();
   load_norm_weights(a.norm, s_w);
+  load_frequencies(a.rope, s_freq);
   __syncthreads();
 
   RowCoef coef;
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
         if (tok + items.step < end) next_pos = a.pos[tok + items.step];
         bad = bad_rope_position(pos);
         if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
-        rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+        rope_angles(a.rope, s_freq, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
       }
       row_coef<INTER>(p, at.is_k && norm, s_w + (at.is_k ? kHeadDim : 0), s_cos[warp],
                       s_sin[warp], coef);
@@ -117,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   __shared__ __align__(16) float s_cos[kWarps][kHalfDim];
   __shared__ __align__(16) float s_sin[kWarps][kHalfDim];
   __shared__ __align__(16) float s_w[2 * kHeadDim];
+  __shared__ double s_freq[kHalfDim];
   __shared__ uint64_t s_dwk[kWarps][8][32];  // a lane's sixteen sums, in pairs
   __shared__ float s_dw[kWarps][2 * kHeadDim];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
 #pragma unroll 1
   for (int i = 0; i < kBwdAhead; ++i) load();
   load_norm_weights(a.norm, s_w);
+  load_frequencies(a.rope, s_freq);
 #pragma unroll
   for (int i = 0; i < 8; ++i) s_dwk[warp][i][lane] = 0;
   __syncthreads();
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
         if (tok + items.step < end) next_pos = a.pos[tok + items.step];
         bad = bad_rope_position(pos);
         if (bad && a.status && lane == 0) atomicOr(a.status, rope_position_flag(pos));
-        rope_angles(a.rope, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
+        rope_angles(a.rope, s_freq, bad ? 0 : pos, lane, s_cos[warp], s_sin[warp]);
         lane_angles(p, s_cos[warp], s_sin[warp], c, s);
       }
       lane_weights<INTER>(s_w + (is_k ? kHeadDim : 0), p, wu, wv);

@@ -11,10 +11,10 @@
 //   interleaved: chunks (l, l + 8); pairs (2i, 2i + 1) never leave a chunk
 // A warp takes four heads of one token at a time; q and k heads are never mixed in one item.
 //
-// A lane's eight pairs (u, v) of queries become rstd (u a - v b), rstd (v c + u d) with coefficients
-// that hold the weights and the angles, a = w_u cos, b = w_v sin, c = w_v cos, d = w_u sin: formed
-// once for all heads of a token, they leave six operations a pair (340 -> 150 instructions per four
-// heads with the loads, where HBM allows 350).
+// A lane's eight pairs (u, v) of queries become rstd (u a - v b), rstd (v c + u d) with
+// coefficients that hold the weights and the angles, a = w_u cos, b = w_v sin, c = w_v cos,
+// d = w_u sin: formed once for all heads of a token (4 us of 34 at 24000 tokens of 8 + 1 heads),
+// they leave six operations a pair.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -130,14 +130,21 @@ __device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
   return (quadrant & 2) ? make_float2(-x, -y) : make_float2(x, y);
 }
 
+// The frequencies into shared memory, by the whole block.  (Every lane wants another one: read
+// from the kernel's arguments, which serve one address at a time, they took 3.6 us of 37 at 24000
+// tokens of 8 + 1 heads.)
+__device__ __forceinline__ void load_frequencies(const RopeArgs& r, double* freq) {
+  if (threadIdx.x < kHalfDim) freq[threadIdx.x] = r.inv_freq[threadIdx.x];
+}
+
 // One warp forms all angles of a token, into its own cos[64], sin[64] in shared memory.
-__device__ __forceinline__ void rope_angles(const RopeArgs& r, int64_t pos, int lane, float* cos,
-                                            float* sin) {
+__device__ __forceinline__ void rope_angles(const RopeArgs& r, const double* freq, int64_t pos,
+                                            int lane, float* cos, float* sin) {
   __syncwarp();  // the last token's are no longer read
 #pragma unroll
   for (int i = lane; i < kHalfDim; i += 32) {
     if (i >= r.dim / 2) break;
-    const float2 cs = cos_sin_of(double(pos), r.inv_freq[i]);
+    const float2 cs = cos_sin_of(double(pos), freq[i]);
     cos[i] = cs.x * r.attn;
     sin[i] = cs.y * r.attn;
   }
@@ -287,7 +294,7 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const floa
 
 // Norm (where `norm`) and rotation of a lane's pairs in place, fp32.  Normalised keys (`key`) are
 // rounded step by step, x rstd, times w, the rotation's products and their sum, as the formula's
-// plain evaluation does: a 4-bit store turns a last bit that differs into a whole code now and then,
+// plain evaluation does: a 4-bit store turns a last bit that differs into a whole code at times,
 // and a token has few key heads.
 __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool key,
                                               const RowCoef& k, float eps, uint64_t (&u)[4],
