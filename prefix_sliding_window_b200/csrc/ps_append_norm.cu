@@ -5,15 +5,15 @@
 // token's position and written to their prefix row or ring slot, values go straight there, queries
 // to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half
 // of them kept: 103 us, 81 % of a copy's rate; into 4 bits 120 us) and by latency for a decode
-// step's single tokens.  Of tokens that share a ring slot only the newest of the call is written, so the
-// result does not depend on which block runs first.
+// step's single tokens.  Of tokens that share a ring slot only the newest of the call is written,
+// so the result does not depend on which block runs first.
 //
 // A warp keeps a token's angles and weights in registers over all of its heads, as in the pass
 // without a store; with few tokens eight warps share one.
 //
-// 4-bit rows: eight lanes hold a row, so the least and greatest value of a group of 64 dims, kept in
-// one word, take three shuffles; every lane packs its two 8-dim chunks into two of the row's sixteen
-// words.
+// 4-bit rows: eight lanes hold a row, so the least and greatest value of a group of 64 dims, kept
+// in one word, take three shuffles; every lane packs its two 8-dim chunks into two of the row's
+// sixteen words.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -36,8 +36,8 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// A chunk's least value and its greatest one's negative, a bf16 each: the least of two such words is
-// both again.
+// A chunk's least value and its greatest one's negative, a bf16 each: the least of two such words
+// is both again.
 __device__ __forceinline__ uint32_t span_word(const uint4& w) {
   const uint32_t lo = min2_nan(min2_nan(w.x, w.y), min2_nan(w.z, w.w));
   const uint32_t hi = max2_nan(max2_nan(w.x, w.y), max2_nan(w.z, w.w));
@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             block = st.table[at_place.b * st.table_stride + (ring ? st.pre_blocks : 0) +
                              store_at / 64];
         }
-        if (!kv || kept) rope_angles(a.rope, s_freq, t.bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
+        if (!kv || kept)
+          rope_angles(a.rope, s_freq, t.bad ? 0 : t.pos, lane, s_cos[warp], s_sin[warp]);
       }
       if (kv && !kept) {  // on to the next token
         at = items.first(tok + items.step);

@@ -683,12 +683,12 @@ __global__ void __launch_bounds__(kMaxGroup * 32) merge_q4_kernel(const DecodeQ4
 }
 
 // In how many blocks a unit is worked on, at most.  Pieces fill the SMs and even out the last wave
-// of blocks, but each starts and ends on its own and has to be merged.  Of the numbers that fill one
-// to eight halves of a wave, the one of least time is taken, with 0.1 us for a tile of each of an
-// SM's two blocks (46 GB/s an SM), 4 us for a block's start and end and 2 us for a merge.  Half a
-// wave of pieces counts as a whole one: behind another kernel some SMs get two of its blocks (74 units of
-// 4196 rows: 21.4 us in two pieces, 16.0 in four; whole units, 40 x 32768 rows: 110.9 us in one
-// piece, 77.3 in seven; 1024 x 8448 rows: 200 in one, 218 in two).
+// of blocks, but each starts and ends on its own and has to be merged.  Of the numbers that fill
+// one to eight halves of a wave, the one of least time is taken, with 0.1 us for a tile of each of
+// an SM's two blocks (46 GB/s an SM), 4 us for a block's start and end and 2 us for a merge.  Half a
+// wave of pieces counts as a whole one: behind another kernel some SMs get two of its blocks (74
+// units of 4196 rows: 21.4 us in two pieces, 16.0 in four).  Whole units: 40 of 32768 rows take
+// 110.9 us in one piece, 77.3 in seven; 1024 of 8448 rows 200 in one, 218 in two.
 int64_t plan_decode(int64_t batch, int32_t hkv, int64_t max_keys) {
   const int64_t units = batch * hkv, sms = sm_count();
   const int64_t tiles = max_keys / kTile + 3;  // (a partial one at the end of each run)
