@@ -324,6 +324,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   }
 }
 
+// x / y in 32 bits where x fits (the case in practice).
+__device__ __forceinline__ int64_t quotient(int64_t x, int32_t y) {
+  return x < (1ll << 32) ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
+}
+
 // Eight lanes a row: lane l takes the 8-dim block l of both groups (words 2 l, 2 l + 1).
 __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
   pdl_wait();
@@ -331,9 +336,9 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(const ReadQ4Args a) {
   const int lane8 = threadIdx.x & 7;
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;  // (b, t, head)
   if (i >= a.batch * a.T * a.hkv) return;
-  const int head = static_cast<int>(i % a.hkv);
-  const int64_t tok = i / a.hkv, b = tok / a.T;
-  const int64_t p0 = a.pos0[b], pos = p0 + tok % a.T;
+  const int64_t tok = quotient(i, a.hkv), b = quotient(tok, a.T);
+  const int head = static_cast<int>(i - tok * a.hkv);
+  const int64_t p0 = a.pos0[b], pos = p0 + (tok - b * a.T);
   const StoreRow row = store_row(a.store, a.hkv, b, pos);
   if (row.flag && a.status && lane8 == 0 && head == 0) atomicOr(a.status, row.flag);
   const bool stale = !a.store.linear && pos >= a.store.lp && pos <= p0 + a.T - 1 - a.store.w;
