@@ -547,3 +547,41 @@ def test_captured_steps_and_streams(cuda_device):
     for s in runs:
         for a, b in zip(s["want"], (s["out"], s["lse"], s["qo"])):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("Bn", [256, 257, 700])
+def test_append_many_sequences(cuda_device, Bn):
+    """More tokens than blocks, from many sequences (some at positions that no store has): the rows
+    and queries of slices of the batch appended one by one."""
+    dev, T, hq, hkv, lp, w = cuda_device, 3, 4, 2, 5, 4
+    params = B.make_params(hq, hkv, D, lp, w, THETA)
+    rope = B.make_rope(params)
+    weights = [(1 + 0.3 * torch.randn(D, generator=torch.Generator().manual_seed(i))).to(dev)
+               for i in (1, 2)]
+    norm = B.make_norm(*weights, EPS)
+    q, k, v = _rows(Bn, T, hq, hkv, 31, dev)
+    pos0 = torch.randint(0, 40, (Bn,), generator=torch.Generator().manual_seed(Bn)).to(dev)
+    pos0[3], pos0[Bn - 2], pos0[Bn - 1] = -2, (1 << 31) - 1, 1 << 40
+    runs = []
+    for step in (Bn, 50):
+        bf = PrefixSlidingCache(Bn, hkv, lp, w, D, dev, fill=9.0)
+        q4 = QuantizedCache(Bn, hkv, lp, w, dev)
+        outs = [torch.full((Bn, T, hq, D), 7.0, dtype=torch.bfloat16, device=dev)
+                for _ in range(2)]
+        st = torch.zeros(2, dtype=torch.int32, device=dev)
+        for b in range(0, Bn, step):
+            e = min(b + step, Bn)
+            c = B.make_cache(*(x[b:e] for x in (bf.k_prefix, bf.v_prefix, bf.k_ring, bf.v_ring)),
+                             e - b)
+            c4 = B.make_cache_q4(*(tuple(x[b:e] for x in p) for p in (q4.prefix, q4.ring)), e - b)
+            B.ps_kv_append_norm_rope(params, rope, norm, c, k[b:e], v[b:e], q[b:e],
+                                     outs[0][b:e], pos0[b:e], T, st[:1])
+            B.ps_kv_append_norm_rope_q4(params, rope, norm, c4, k[b:e], v[b:e], q[b:e],
+                                        outs[1][b:e], pos0[b:e], T, st[1:])
+        runs.append([bf.k_prefix, bf.v_prefix, bf.k_ring, bf.v_ring, *q4.prefix, *q4.ring, *outs,
+                     st])
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+    assert (runs[0][-1] == (B.PS_DEV_BAD_POS | B.PS_DEV_POS_RANGE)).all()
+    assert (runs[0][-2][Bn - 1] == 0).all() and (runs[0][-2][3, :2] == 0).all()
+    assert (runs[0][-2][3, 2] != 0).any()     # position 0
