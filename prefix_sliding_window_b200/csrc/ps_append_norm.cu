@@ -4,7 +4,7 @@
 // One pass: a token's packed q, k and v heads are read once; keys are normalised, rotated at the
 // token's position and written to their prefix row or ring slot, values go straight there, queries
 // to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half
-// of them kept: 103 us, 81 % of a copy's rate; into 4 bits 120 us) and by latency for a decode
+// of them kept: 96 us, 88 % of a copy's rate; into 4 bits 113 us) and by latency for a decode
 // step's single tokens.  Of tokens that share a ring slot only the newest of the call is written,
 // so the result does not depend on which block runs first.
 //
@@ -115,7 +115,7 @@ __device__ __forceinline__ void quantise_row(const RopeLane& p, const uint4& r1,
         make_uint2(cvt_bf16x2(s[0], m[0]), cvt_bf16x2(s[1], m[1]));
 }
 
-constexpr int kAhead = 4;  // items in flight a warp
+constexpr int kAhead = 2;  // items in flight a warp (four: 1 % slower)
 constexpr int kBlocksPerSm = 2;
 // Start positions of up to this many sequences are kept in shared memory (every warp reads its
 // tokens' twice; from L2 they cost 1 us of 114 at 4 x 8192 tokens).

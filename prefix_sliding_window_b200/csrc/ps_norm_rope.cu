@@ -9,8 +9,8 @@
 // prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
 // 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
 //
-// At 4 x 8192 tokens of 28 + 4 heads the forward takes 89 us (6.0 TB/s, 93 % of a copy's rate), the
-// backward 132 us (95 %).  Three blocks of 80 registers an SM: 97 and more.
+// At 4 x 8192 tokens of 28 + 4 heads the forward takes 86 us (6.3 TB/s, 97 % of a copy's rate), the
+// backward 131 us (95 %).  Three blocks of 80 registers an SM: 97 and more.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -20,8 +20,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlocksPerSm = 2, kAhead = 4;  // items in flight a warp, forward
-constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 2;  // backward: an item is twice the bytes
+// Items in flight a warp: forward two (four: 97 us where these take 86), backward two, each twice
+// the bytes.
+constexpr int kBlocksPerSm = 2, kAhead = 2;
+constexpr int kBwdBlocksPerSm = 2, kBwdAhead = 2;
 
 // Warps stride over tokens; SPLIT of them share one (1 or 8) and take its items in turn.
 template <int SPLIT, bool INTER>
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
       uint64_t gu[4], gv[4];
       unpack_pairs<INTER>(r[0], r[32], gu, gv);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)  // (a branch for heads rotated whole, as forward: 3 % slower)
         if (i < 2 ? p.rot1 : p.rot2) {
           const uint64_t x = gu[i], y = gv[i];
           gu[i] = ffma2(y, s[i], fmul2(x, c[i]));

@@ -33,11 +33,13 @@ struct RopeLane {
   int c1, c2;       // chunks (dims 8 c .. 8 c + 7)
   int a1, a2;       // angles of pairs 0..3 start at a1, of 4..7 at a2
   bool rot1, rot2;  // whether pairs 0..3 and 4..7 are rotated
+  bool all;         // whether every lane's are
 };
 
 template <bool INTER>
 __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   RopeLane p;
+  p.all = r.dim == kHeadDim;
   if (INTER) {
     p.c1 = l;
     p.c2 = l + 8;
@@ -292,10 +294,44 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const floa
   }
 }
 
-// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.  Normalised keys (`key`) are
-// rounded step by step, x rstd, times w, the rotation's products and their sum, as the formula's
-// plain evaluation does: a 4-bit store turns a last bit that differs into a whole code at times,
-// and a token has few key heads.
+// Normalised keys are rounded step by step, x rstd, times w, the rotation's products and their sum,
+// as the formula's plain evaluation does: a 4-bit store turns a last bit that differs into a whole
+// code at times, and a token has few key heads.  ALL: every pair is rotated (asked per pair it costs
+// an eighth of the forward's instructions; a pair that is not must not see the other's infinity).
+template <bool ALL>
+__device__ __forceinline__ void norm_and_turn_key(const RopeLane& p, const RowCoef& k, uint64_t r2,
+                                                  uint64_t (&u)[4], uint64_t (&v)[4]) {
+  const uint64_t minus = pack_f32x2(-1.f, -1.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint64_t x = fmul2_rn(fmul2_rn(u[i], r2), k.a[i]);
+    uint64_t y = fmul2_rn(fmul2_rn(v[i], r2), k.c[i]);
+    if (ALL || (i < 2 ? p.rot1 : p.rot2)) {
+      const uint64_t xs = fmul2_rn(x, k.d[i]), ys = fmul2_rn(y, k.d[i]);
+      x = ffma2(ys, minus, fmul2_rn(x, k.b[i]));
+      y = fadd2(fmul2_rn(y, k.b[i]), xs);
+    }
+    u[i] = x;
+    v[i] = y;
+  }
+}
+template <bool ALL>
+__device__ __forceinline__ void norm_and_turn_query(const RopeLane& p, const RowCoef& k,
+                                                    uint64_t r2, uint64_t (&u)[4],
+                                                    uint64_t (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint64_t x = fmul2(u[i], k.a[i]), y = fmul2(v[i], k.c[i]);
+    if (ALL || (i < 2 ? p.rot1 : p.rot2)) {
+      x = ffma2(v[i], k.b[i], x);
+      y = ffma2(u[i], k.d[i], y);
+    }
+    u[i] = fmul2(x, r2);
+    v[i] = fmul2(y, r2);
+  }
+}
+
+// Norm (where `norm`) and rotation of a lane's pairs in place, fp32.
 __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool key,
                                               const RowCoef& k, float eps, uint64_t (&u)[4],
                                               uint64_t (&v)[4]) {
@@ -303,30 +339,11 @@ __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool
     const float rstd = row_rstd(u, v, eps);
     const uint64_t r2 = pack_f32x2(rstd, rstd);
     if (key) {
-      const uint64_t minus = pack_f32x2(-1.f, -1.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint64_t x = fmul2_rn(fmul2_rn(u[i], r2), k.a[i]);
-        uint64_t y = fmul2_rn(fmul2_rn(v[i], r2), k.c[i]);
-        if (i < 2 ? p.rot1 : p.rot2) {
-          const uint64_t xs = fmul2_rn(x, k.d[i]), ys = fmul2_rn(y, k.d[i]);
-          x = ffma2(ys, minus, fmul2_rn(x, k.b[i]));
-          y = fadd2(fmul2_rn(y, k.b[i]), xs);
-        }
-        u[i] = x;
-        v[i] = y;
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint64_t x = fmul2(u[i], k.a[i]), y = fmul2(v[i], k.c[i]);
-      if (i < 2 ? p.rot1 : p.rot2) {  // (an infinity reaches its own pair only)
-        x = ffma2(v[i], k.b[i], x);
-        y = ffma2(u[i], k.d[i], y);
-      }
-      u[i] = fmul2(x, r2);
-      v[i] = fmul2(y, r2);
+      if (p.all) norm_and_turn_key<true>(p, k, r2, u, v);
+      else norm_and_turn_key<false>(p, k, r2, u, v);
+    } else {
+      if (p.all) norm_and_turn_query<true>(p, k, r2, u, v);
+      else norm_and_turn_query<false>(p, k, r2, u, v);
     }
   } else {
 #pragma unroll
