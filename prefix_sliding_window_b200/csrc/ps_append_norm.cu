@@ -4,7 +4,7 @@
 // One pass: a token's packed q, k and v heads are read once; keys are normalised, rotated at the
 // token's position and written to their prefix row or ring slot, values go straight there, queries
 // to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half
-// of them kept: 96 us, 88 % of a copy's rate; into 4 bits 113 us) and by latency for a decode
+// of them kept: 97 us, 86 % of a copy's rate; into 4 bits 115 us) and by latency for a decode
 // step's single tokens.  Of tokens that share a ring slot only the newest of the call is written,
 // so the result does not depend on which block runs first.
 //
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     uint4 y1, y2;
     const bool live = row < at.rows && (!kv || writes);
     if (!kv) {
-      norm_and_turn(p, norm, false, coef, a.norm.eps, u, v);
+      norm_and_turn<INTER>(p, norm, false, coef, a.norm.eps, u, v);
       pack_pairs<INTER>(u, v, y1, y2);
       if (skip) y1 = y2 = make_uint4(0, 0, 0, 0);
       if (live) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
       dst += items.kStride;
     } else {
-      norm_and_turn(p, norm, true, coef, a.norm.eps, u, v);
+      norm_and_turn<INTER>(p, norm, true, coef, a.norm.eps, u, v);
       pack_pairs<INTER>(u, v, y1, y2);
       const int r = 2 * a.hkv - at.rows + row;
       const bool is_v = r >= a.hkv;

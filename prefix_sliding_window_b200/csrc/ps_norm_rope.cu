@@ -10,7 +10,7 @@
 // 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
 //
 // At 4 x 8192 tokens of 28 + 4 heads the forward takes 86 us (6.3 TB/s, 97 % of a copy's rate), the
-// backward 131 us (95 %).  Three blocks of 80 registers an SM: 97 and more.
+// backward 132 us (94 %).  Three blocks of 80 registers an SM: 97 and more.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     const uint4* r = &s_ring[warp][0][0][lane] + out / sizeof(uint4);
     unpack_pairs<INTER>(r[0], r[32], u, v);
     out = out == kRing - kItem ? 0 : out + kItem;
-    norm_and_turn(p, norm, at.is_k, coef, a.norm.eps, u, v);
+    norm_and_turn<INTER>(p, norm, at.is_k, coef, a.norm.eps, u, v);
     uint4 y1, y2;
     pack_pairs<INTER>(u, v, y1, y2);
     if (bad) y1 = y2 = make_uint4(0, 0, 0, 0);

@@ -34,12 +34,14 @@ struct RopeLane {
   int a1, a2;       // angles of pairs 0..3 start at a1, of 4..7 at a2
   bool rot1, rot2;  // whether pairs 0..3 and 4..7 are rotated
   bool all;         // whether every lane's are
+  bool halves;      // whether every lane's chunks are eight apart
 };
 
 template <bool INTER>
 __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   RopeLane p;
   p.all = r.dim == kHeadDim;
+  p.halves = INTER || p.all;
   if (INTER) {
     p.c1 = l;
     p.c2 = l + 8;
@@ -106,8 +108,9 @@ __device__ __forceinline__ void pack_pairs(const uint64_t (&u)[4], const uint64_
 
 // cos and sin of p * inv_f: reduced to [-pi/4, pi/4] in float64 (pi/2 in two parts; the first
 // difference is exact, so the remainder is good to 2^-53 of pi/2 beside the product's own
-// rounding), then Taylor sums in fp32, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9) before
-// roundings.  30 instructions where the library's other rotations, through sincosf, take 240: with
+// rounding), then Taylor sums, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9): what is added to
+// the first terms in fp32, the sum in float64, so that nearly all results are the correctly rounded
+// ones.  40 instructions where the library's other rotations, through sincosf, take 240: with
 // 16 + 2 heads a token's 64 angles were a fifth of the forward's time (73 us at 32768 tokens, 64
 // with these).
 __device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
@@ -118,16 +121,16 @@ __device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
   const double k = t - shifter;
   double red = fma(-k, 1.5707963267948965580, ang);
   red = fma(-k, 6.1232339957367660359e-17, red);
-  const float r = static_cast<float>(red), r2 = r * r;
+  const double red2 = red * red;
+  const float r2 = static_cast<float>(red2);
   float s = fmaf(r2, 1.f / 362880.f, -1.f / 5040.f);
   s = fmaf(s, r2, 1.f / 120.f);
-  s = fmaf(s, r2, -1.f / 6.f);
-  s = fmaf(s, r * r2, r);
+  s = fmaf(s, r2, -1.f / 6.f) * r2;
+  s = static_cast<float>(fma(red, static_cast<double>(s), red));
   float c = fmaf(r2, -1.f / 3628800.f, 1.f / 40320.f);
   c = fmaf(c, r2, -1.f / 720.f);
-  c = fmaf(c, r2, 1.f / 24.f);
-  c = fmaf(c, r2, -0.5f);
-  c = fmaf(c, r2, 1.f);
+  c = fmaf(c, r2, 1.f / 24.f) * (r2 * r2);
+  c = static_cast<float>(1.0 + fma(red2, -0.5, static_cast<double>(c)));
   const float x = (quadrant & 1) ? -s : c, y = (quadrant & 1) ? c : s;
   return (quadrant & 2) ? make_float2(-x, -y) : make_float2(x, y);
 }
@@ -215,6 +218,35 @@ __device__ __forceinline__ float row_rstd(const uint64_t (&u)[4], const uint64_t
   return rsqrtf(row_sum(x.x + x.y) * (1.f / kHeadDim) + eps);
 }
 
+// The same, with the squares summed four neighbours in turn, then halves onto halves (where
+// p.halves): the order of a plain evaluation's sum.
+template <bool INTER>
+__device__ __forceinline__ float row_rstd_by_halves(const uint64_t (&u)[4], const uint64_t (&v)[4],
+                                                    float eps) {
+  float part[2][2];  // [chunk][first or second four dims]
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float2 a, b;
+      if (INTER) {
+        const float2 x = unpack_f32x2(u[2 * c + h]), y = unpack_f32x2(v[2 * c + h]);
+        a = make_float2(x.x, y.x), b = make_float2(x.y, y.y);
+      } else {
+        a = unpack_f32x2(c ? v[2 * h] : u[2 * h]);
+        b = unpack_f32x2(c ? v[2 * h + 1] : u[2 * h + 1]);
+      }
+      part[c][h] = fmaf(b.y, b.y, fmaf(b.x, b.x, fmaf(a.y, a.y, a.x * a.x)));
+    }
+  float s0 = part[0][0] + part[1][0], s1 = part[0][1] + part[1][1];
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+  }
+  return rsqrtf((s0 + s1) * (1.f / kHeadDim) + eps);
+}
+
 // The norm's weights as fp32 in shared memory: [0, 128) queries, [128, 256) keys (1 where there
 // is none, and then no norm is applied).
 __device__ __forceinline__ void load_norm_weights(const NormArgs& n, float* s_w) {
@@ -296,7 +328,8 @@ __device__ __forceinline__ void row_coef(const RopeLane& p, bool key, const floa
 
 // Normalised keys are rounded step by step, x rstd, times w, the rotation's products and their sum,
 // as the formula's plain evaluation does: a 4-bit store turns a last bit that differs into a whole
-// code at times, and a token has few key heads.  ALL: every pair is rotated (asked per pair it costs
+// code at times (of 9 million codes ten with folded coefficients, none or one so), and a token has
+// few key heads.  ALL: every pair is rotated (asked per pair it costs
 // an eighth of the forward's instructions; a pair that is not must not see the other's infinity).
 template <bool ALL>
 __device__ __forceinline__ void norm_and_turn_key(const RopeLane& p, const RowCoef& k, uint64_t r2,
@@ -332,11 +365,13 @@ __device__ __forceinline__ void norm_and_turn_query(const RopeLane& p, const Row
 }
 
 // Norm (where `norm`) and rotation of a lane's pairs in place, fp32.
+template <bool INTER>
 __device__ __forceinline__ void norm_and_turn(const RopeLane& p, bool norm, bool key,
                                               const RowCoef& k, float eps, uint64_t (&u)[4],
                                               uint64_t (&v)[4]) {
   if (norm) {
-    const float rstd = row_rstd(u, v, eps);
+    const float rstd =
+        key && p.halves ? row_rstd_by_halves<INTER>(u, v, eps) : row_rstd(u, v, eps);
     const uint64_t r2 = pack_f32x2(rstd, rstd);
     if (key) {
       if (p.all) norm_and_turn_key<true>(p, k, r2, u, v);
