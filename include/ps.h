@@ -281,10 +281,12 @@ size_t ps_decode_q4_workspace_bytes(const ps_params* params, int64_t batch);
  * values its visible rows stand for.  In a linear store (ring NULL) the query at pos[b] sees
  * [0, pos[b]], and pos[b] >= l_prefix is skipped (PS_DEV_POS_RANGE).  Rows no visible position
  * maps to may hold anything.  A block table entry outside [0, n_blocks) sets PS_DEV_POS_RANGE
- * and that block's rows are left out.  V's scales may lie between 2^-60 and 2^80 (smaller ones
- * lose bits, as values that all are below 1e-17 would), its constant groups below 2^30.  Other
- * arguments, results and errors as ps_decode_attn; the workspace is
- * ps_decode_q4_workspace_bytes(), 16-byte aligned, and of one call at a time. */
+ * and that block's rows are left out.  Positions reach 2^31 - 1, as the append's
+ * (PS_DEV_POS_RANGE above).  Values have to be below 2^90 in magnitude; they may differ
+ * by any factor from row to row and between the groups of a row.  A visible group that stands for NaN makes what it reaches NaN:
+ * of K its head's outputs and lse, of V that group's dims.  Other arguments, results and errors as
+ * ps_decode_attn; the workspace is ps_decode_q4_workspace_bytes(), 16-byte aligned, and of one call
+ * at a time. */
 int ps_decode_attn_q4(const ps_params* params, const ps_kv_cache_q4* cache, const void* q,
                       const int64_t* pos, void* out, float* lse, void* workspace,
                       size_t ws_bytes, int32_t* dev_status, ps_stream_t stream);

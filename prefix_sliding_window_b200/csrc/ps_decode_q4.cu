@@ -13,9 +13,13 @@
 //    more to bring two rows together.  (As e4m3 bytes a word would cost three operations, but there
 //    is no such warp product in hardware: it is unpacked to halves, 186 us where this took 139 at
 //    256 sequences of 28 / 4 heads and 4196 rows)
-//  * queries are bf16 as given, times 2^64 against the small codes; weights are fp16, on a scale
-//    that keeps the greatest weight times V scale in [2^6, 2^14): 11 bits down to 2^-20 of the
-//    greatest.  (As bf16 their 8 bits tripled the output's error, since codes are not centred)
+//  * queries are bf16 as given, times 2^64 against the small codes
+//  * a weight times its row's V scale is rounded to fp16, on a power of two of its own for every
+//    query head and group that follows the greatest such product: 11 bits down to 2^-10 of the
+//    greatest at least, off by 2^-21 of it at most below.  (On one scale for all, set by the
+//    greatest V scale, a group whose scales are 2^-24 of the other's lost bits, one of 2^-32 all of
+//    them.  As bf16 the products' 8 bits tripled the output's error, since codes are not centred;
+//    centring them, by a product with a constant 8 a group, takes 13 % more time)
 //  * the dims of a row are stored so that one 16-byte load gives a lane the words of a whole
 //    K fragment row; which dim goes to which position of the product does not matter as long as
 //    the query's fragment agrees
@@ -63,14 +67,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLift = 18446744073709551616.f;     // 2^64: queries, against the codes' 2^-133
 constexpr float kUncode = 590295810358705651712.f;  // 2^69 = 2^133 / 2^64
 constexpr float kUncodeV = 16777216.f;              // 2^24
-// A weight times its row's V scale is below 2^(kWeightLog2 + kMaxSlack) = 2^14 < 65504.
-constexpr int kWeightLog2 = 6;
-// V scales below 2^kLeastScale count as that: weights stay below 2^74, and fp32 sums of them times
-// values finite, where all groups so far were constant (s = 0) and below 2^30.
-constexpr int kLeastScale = -60;
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
-constexpr float kMaxSlack = 8.f;
+constexpr int kMaxSlack = 8;
+// Of a head and group, products of a weight and a V scale go to fp16 times 2^e.  Where e is set, R
+// being the greatest product so far (or a bound below it), R 2^e is in [2^(kProductLeast - 1),
+// 2^kProductMost).  Until it is set again products stay below 2^kOperandMost: weights are below
+// 2^kMaxSlack, and a V scale of 2^(kOperandMost - kMaxSlack - e) or more sets it again, low enough
+// for that scale if the range allows it.  (Low only then: what is below 2^-14 loses bits.)
+constexpr int kOperandMost = 15, kProductMost = 4, kProductLeast = -3;
+// |e| is at most this: a weight times 2^e stays finite, 2^-e normal.
+constexpr int kExpMost = 116;
 
 struct DecodeQ4Args {
   const __nv_bfloat16* q;
@@ -250,6 +257,17 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// Products of two bf16 pairs, and the greater sizes of each half (a NaN counts for nothing).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b & 0x7fff7fffu));
+  return d;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -278,10 +296,17 @@ __device__ __forceinline__ float hi_f(uint32_t w) {
   return y;
 }
 
+// 2^e, |e| <= 126, and back.
+__device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ int exp_of(float x) {
+  return static_cast<int>(__float_as_uint(x) >> 23) - 127;
+}
+
 // One warp's running softmax and accumulators over the heads (2 t, 2 t + 1) of its lane's t.
 struct State {
   float l[2];
-  float o[8][4];   // tile 4 g + i: dims 64 g + 8 (lane / 4) + 2 i + {0, 1}, heads 2 t + {0, 1}
+  float o[8][4];   // tile 4 g + i: dims 64 g + 8 (lane / 4) + 2 i + {0, 1}, heads 2 t + {0, 1};
+                   // times 2^e of the group and head
   float mn[2][2];  // sum p m of a group, over this lane's rows
 };
 
@@ -324,7 +349,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
   const int head0 = b * a.hq + h * a.group;
 
   // scores come out of the products times 2^(64 - 133); c takes that off and scales to base 2
-  const float c = a.scale_log2 * kUncode;
+  const float c = a.scale_log2 * kUncode, to_x = 1.f / c;
   Cursor cursor{nullptr, nullptr, nullptr, 0};
   const uint32_t mine = smem_u32(stages) + lane * 16;
   uint32_t tile = warp;  // the warp's next to load
@@ -394,10 +419,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
   st.mn[0][0] = st.mn[0][1] = st.mn[1][0] = st.mn[1][1] = 0.f;
   // a score (before c) above this moves the running maximum m
   float above[2] = {-INFINITY, -INFINITY};
-  // weights are 2^(c x + shift), shift = kWeightLog2 - m - log2 of the least power of two above
-  // every V scale so far (while there is no m, no score counts)
+  // weights are 2^(c x + shift), shift = -m, m whole (while there is no m, no score counts)
   float shift[2] = {INFINITY, INFINITY};
-  int scale_exp = kLeastScale;
+  // 2^e of both groups, of the two heads as a pair, and the greatest V scales of the two groups
+  // that do not set it again, as bf16 side by side
+  uint64_t lift[2];
+  lift[0] = lift[1] = pack_f32x2(exp2_of(kExpMost), exp2_of(kExpMost));
+  uint32_t scales_below = 0;
 
   const int kr = tile_row(g8);  // this lane's K rows: kr, kr + 8
   uint32_t at = 0;  // the stage of the tile in hand
@@ -459,38 +487,78 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       mx[e] = fmaxf(max3f(x[0][e], x[0][2 + e], x[1][e]), x[1][2 + e]);
-    // this lane looks at row `lane`'s V scales (bf16, not negative: they compare as integers)
+    // this lane looks at row `lane`'s V scales (bf16: not negative, they compare as integers)
     const uint2 own = *reinterpret_cast<const uint2*>(stage + 2 * kTile * kQ4RowBytes +
                                                       lane * kQ4RecordBytes + 8);
-    const uint32_t top = max_u16x2(own.x, own.y) & 0xffffu;
+    const uint32_t scales = __byte_perm(own.x, own.y, 0x5410);
     if (__any_sync(0xffffffffu, mx[0] > above[0] || mx[1] > above[1] ||
-                                    top >= static_cast<uint32_t>(scale_exp + 127) << 7)) {
-      // (a scale that is not finite makes its products NaN whatever the exponent)
-      const uint32_t most = __reduce_max_sync(0xffffffffu, top < 0x7f80u ? top : 0u);
-      const int was = scale_exp;
-      scale_exp = max(scale_exp, static_cast<int>(most >> 7) - 126);
-      float f[2];
+                                    max_u16x2(scales, scales_below) != scales_below)) {
+      int fall[2];  // log2 of what weights so far shrink by
+      float sh[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-        // the old m, from the old shift (-inf where there is none)
-        const float m = fmaxf(static_cast<float>(kWeightLog2 - was) - shift[e], mx[e] * c);
-        const float to = static_cast<float>(kWeightLog2 - scale_exp) - m;
-        f[e] = shift[e] == INFINITY ? 0.f : fast_exp2(to - shift[e]);
-        if (m != -INFINITY) above[e] = (m + kMaxSlack) / c;
-        shift[e] = to;
-        st.l[e] *= f[e];
-        st.mn[0][e] *= f[e];
-        st.mn[1][e] *= f[e];
+        const float m = fmaxf(-shift[e], ceilf(mx[e] * c));  // (-inf where there is none)
+        fall[e] = 0;
+        sh[e] = 0.f;
+        if (m != -INFINITY) {
+          const float x_most = (m + kMaxSlack) * to_x;
+          above[e] = fmaf(-0x1p-20f, fabsf(x_most), x_most);  // (less what its roundings may add)
+          fall[e] = static_cast<int>(fminf(m + shift[e], 1000.f));
+          sh[e] = -m;
+        }
+        shift[e] = -m;
+        const float f = fast_exp2(static_cast<float>(-fall[e]));
+        st.l[e] *= f;
+        st.mn[0][e] *= f;
+        st.mn[1][e] *= f;
       }
+      // each group's greatest products of both heads, as bf16
+      uint32_t most[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        st.o[j][0] *= f[0];
-        st.o[j][1] *= f[1];
-        st.o[j][2] *= f[0];
-        st.o[j][3] *= f[1];
+      for (int r = 0; r < 4; ++r) {
+        const float* y = &x[r >> 1][2 * (r & 1)];
+        const uint32_t p = cvt_bf16x2(fast_exp2(fmaf(y[0], c, sh[0])),
+                                      fast_exp2(fmaf(y[1], c, sh[1])));
+        const uint2 k = *reinterpret_cast<const uint2*>(rec + 8 * r * kQ4RecordBytes + 8);
+        most[0] = max_abs_bf16x2(most[0], mul_bf16x2(p, __byte_perm(k.x, 0, 0x1010)));
+        most[1] = max_abs_bf16x2(most[1], mul_bf16x2(p, __byte_perm(k.y, 0, 0x1010)));
+      }
+      scales_below = 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          most[g] = max_u16x2(most[g], __shfl_xor_sync(0xffffffffu, most[g], o));
+        // this tile's V scales are below 2^(top - 126)
+        const uint32_t top =
+            __reduce_max_sync(0xffffffffu, (g ? own.y : own.x) & 0x7fffu) >> 7;
+        const float2 lifts = unpack_f32x2(lift[g]);
+        int n[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // the range of e: R is below 2^(b - 126) of this tile's b, and of earlier products one is
+          // 2^(kProductLeast - 1 - was) at least; it rises only as far as weights fall.  (Numbers
+          // that are not finite stay so whatever e is)
+          const int was = exp_of(e ? lifts.y : lifts.x) + fall[e];
+          const int b = (e ? most[g] >> 16 : most[g] & 0xffffu) >> 7;
+          const int least = min(kProductLeast + 126 - b, was);
+          n[e] = max(kOperandMost - kMaxSlack + 126 - static_cast<int>(top), least);
+          n[e] = min(min(n[e], least + kProductMost - kProductLeast), was);
+          n[e] = min(max(n[e], -kExpMost), kExpMost);
+          const float f = fast_exp2(static_cast<float>(n[e] - was));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            st.o[4 * g + i][e] *= f;
+            st.o[4 * g + i][2 + e] *= f;
+          }
+        }
+        lift[g] = pack_f32x2(exp2_of(n[0]), exp2_of(n[1]));
+        // bf16 numbers below 2^(kOperandMost - kMaxSlack - e)
+        const int highest = __reduce_max_sync(0xffffffffu, max(n[0], n[1]));
+        scales_below |= ((min(127 + kOperandMost - kMaxSlack - highest, 254) << 7) - 1) << (16 * g);
       }
     }
     const float sh[2] = {shift[0] == INFINITY ? 0.f : shift[0],
@@ -514,9 +582,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const uint32_t k0 = g ? c0.y : c0.x, k1 = g ? c1.y : c1.x;
-        // a weight times its row's scale, rounded to fp16: the tensor cores' operand type
-        const uint32_t b0 = transpose8(cvt_f16x2(p[0] * lo_f(k0), p[1] * lo_f(k0)));
-        const uint32_t b1 = transpose8(cvt_f16x2(p[2] * lo_f(k1), p[3] * lo_f(k1)));
+        // a weight times its row's scale and 2^e, rounded to fp16: the tensor cores' operand type
+        const float2 w0 = unpack_f32x2(fmul2(pack_f32x2(p[0], p[1]), lift[g]));
+        const float2 w1 = unpack_f32x2(fmul2(pack_f32x2(p[2], p[3]), lift[g]));
+        const uint32_t b0 = transpose8(cvt_f16x2(w0.x * lo_f(k0), w0.y * lo_f(k0)));
+        const uint32_t b1 = transpose8(cvt_f16x2(w1.x * lo_f(k1), w1.y * lo_f(k1)));
         st.mn[g][0] = fmaf(p[0], hi_f(k0), fmaf(p[2], hi_f(k1), st.mn[g][0]));
         st.mn[g][1] = fmaf(p[1], hi_f(k0), fmaf(p[3], hi_f(k1), st.mn[g][1]));
         const uint32_t x0 = g ? v0.y : v0.x, x1 = g ? v1.y : v1.x;
@@ -551,11 +621,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
     float* dst = res + (2 * t4 + e) * kHeadDim + 8 * g8;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
+      const float2 up = unpack_f32x2(lift[g]);
+      const float down = exp2_of(-exp_of(e ? up.y : up.x));
       float y[8];
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
         const int i = 4 * g + (d >> 1), j = 2 * (d & 1) + e;
-        y[d] = fmaf(st.o[i][j], (d & 2) ? kUncodeV / 16.f : kUncodeV, st.mn[g][e]);
+        y[d] = fmaf(st.o[i][j] * ((d & 2) ? kUncodeV / 16.f : kUncodeV), down, st.mn[g][e]);
       }
       reinterpret_cast<float4*>(dst + 64 * g)[0] = make_float4(y[0], y[1], y[2], y[3]);
       reinterpret_cast<float4*>(dst + 64 * g)[1] = make_float4(y[4], y[5], y[6], y[7]);
