@@ -282,8 +282,9 @@ size_t ps_decode_q4_workspace_bytes(const ps_params* params, int64_t batch);
  * [0, pos[b]], and pos[b] >= l_prefix is skipped (PS_DEV_POS_RANGE).  Rows no visible position
  * maps to may hold anything.  A block table entry outside [0, n_blocks) sets PS_DEV_POS_RANGE
  * and that block's rows are left out.  Positions reach 2^31 - 1, as the append's
- * (PS_DEV_POS_RANGE above).  Values have to be below 2^90 in magnitude; they may differ
- * by any factor from row to row and between the groups of a row.  A visible group that stands for NaN makes what it reaches NaN:
+ * (PS_DEV_POS_RANGE above).  Queries have to be below 2^79 in magnitude, values below 2^90 and
+ * softmax_scale at most 2^32 (PS_ERR_UNSUPPORTED); values may differ by any factor from row to row
+ * and between the groups of a row.  A visible group that stands for NaN makes what it reaches NaN:
  * of K its head's outputs and lse, of V that group's dims.  Other arguments, results and errors as
  * ps_decode_attn; the workspace is ps_decode_q4_workspace_bytes(), 16-byte aligned, and of one call
  * at a time. */

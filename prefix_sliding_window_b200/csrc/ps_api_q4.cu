@@ -488,6 +488,8 @@ int ps_decode_attn_q4(const ps_params* params, const ps_kv_cache_q4* cache, cons
   l.hq = params->n_q_heads;
   l.hkv = params->n_kv_heads;
   l.scale = resolve_scale(params);
+  if (l.scale > 0x1p32f)  // (scores come out of the products times 2^-85)
+    return fail(PS_ERR_UNSUPPORTED, "softmax_scale must be <= 2^32");
   return launch_decode_q4(l, as_stream(stream));
 }
 

@@ -13,7 +13,7 @@
 //    more to bring two rows together.  (As e4m3 bytes a word would cost three operations, but there
 //    is no such warp product in hardware: it is unpacked to halves, 186 us where this took 139 at
 //    256 sequences of 28 / 4 heads and 4196 rows)
-//  * queries are bf16 as given, times 2^64 against the small codes
+//  * queries are bf16 as given, times 2^48 against the small codes
 //  * a weight times its row's V scale is rounded to fp16, on a power of two of its own for every
 //    query head and group that follows the greatest such product: 11 bits down to 2^-10 of the
 //    greatest at least, off by 2^-21 of it at most below.  (On one scale for all, set by the
@@ -64,9 +64,11 @@ static_assert(kStageBytes >= (kHeadDim + 2) * kMaxGroup * 4, "a warp's result fi
 constexpr int kGrain = kWarps;  // least tiles of a piece, on average
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLift = 18446744073709551616.f;     // 2^64: queries, against the codes' 2^-133
-constexpr float kUncode = 590295810358705651712.f;  // 2^69 = 2^133 / 2^64
-constexpr float kUncodeV = 16777216.f;              // 2^24
+// Queries times this, against the codes' 2^-133: queries below 2^79 stay finite, and a product's
+// place below the normal numbers, 2^-149, is 2^-64 of a query times a code.
+constexpr float kLift = 281474976710656.f;                  // 2^48
+constexpr float kUncode = 38685626227668133590597632.f;     // 2^85 = 2^133 / 2^48
+constexpr float kUncodeV = 16777216.f;                      // 2^24
 // A running maximum is moved only when a score passes it by more than this (in log2): weights
 // then stay below 2^8, and a row of tiles rarely rescales its accumulators.
 constexpr int kMaxSlack = 8;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
   }
   const int head0 = b * a.hq + h * a.group;
 
-  // scores come out of the products times 2^(64 - 133); c takes that off and scales to base 2
+  // scores come out of the products times 2^(48 - 133); c takes that off and scales to base 2
   const float c = a.scale_log2 * kUncode, to_x = 1.f / c;
   Cursor cursor{nullptr, nullptr, nullptr, 0};
   const uint32_t mine = smem_u32(stages) + lane * 16;
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
     copies_commit();
   };
 
-  // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^64 (2^60
+  // the query's fragments: head g8, blocks 2 t and 2 t + 1 of both groups, times 2^48 (2^44
   // where the codes come out 16 times as large); and each group's sum of query dims
   uint32_t qf[2][2][4];
   float Q[2][2];  // of heads 2 t + e, on the products' scale

@@ -139,6 +139,17 @@ def test_constant_groups_of_any_size(cuda_device, value):
     _run(dev, 8, 1, part, q, [n, 40], value)
 
 
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 66, 2.0 ** -40])
+def test_queries_of_any_size(cuda_device, size):
+    """Large queries (keys scaled down against them) and tiny ones."""
+    dev, n = cuda_device, 600
+    part = _random_store(1, 2, n, 12, dev)
+    rec = part[2].view(1, 2, n, 4, 2)
+    rec[..., :2, :] = (rec[..., :2, :].double() / size).bfloat16()
+    q = (synth.normal_bf16((1, 4, D), 13, dev).double() * size).bfloat16()
+    _run(dev, 4, 2, part, q, [n], size)
+
+
 def test_rows_that_are_not_numbers(cuda_device):
     """A visible row with a NaN group in V makes that group's outputs NaN and no other; one in K all
     of its head's; the same row out of sight changes nothing."""
