@@ -256,7 +256,9 @@ def make_params(n_q_heads, n_kv_heads, head_dim=128, l_prefix=0, window=1, rope_
 
 
 def make_cache(k_prefix, v_prefix, k_ring, v_ring, batch: int) -> PsKVCache:
-    return PsKVCache(_ptr(k_prefix), _ptr(v_prefix), _ptr(k_ring), _ptr(v_ring), int(batch))
+    cache = PsKVCache(_ptr(k_prefix), _ptr(v_prefix), _ptr(k_ring), _ptr(v_ring), int(batch))
+    cache.held = (k_prefix, v_prefix, k_ring, v_ring)  # the struct keeps only addresses
+    return cache
 
 
 _ROPE_LAYOUTS = {"half": PS_ROPE_HALF, "interleaved": PS_ROPE_INTERLEAVED}
@@ -299,6 +301,11 @@ def make_cache_q4(prefix, ring, batch: int, block_table=None) -> PsKVCacheQ4:
     holds the pools, ring is None and block_table [batch, stride] int32 is given."""
     import torch
     held = [t for part in (prefix, ring) if part is not None for t in part]
+    if block_table is not None:
+        held.append(block_table)
+    for t in held:
+        if t.get_device() != held[0].get_device():
+            raise ValueError("the parts of a 4-bit store are on one device")
     for part in (prefix, ring):
         for t, dtype, width in zip(part or (), (torch.uint8, torch.uint8, torch.bfloat16),
                                    (64, 64, 8)):
@@ -314,13 +321,57 @@ def make_cache_q4(prefix, ring, batch: int, block_table=None) -> PsKVCacheQ4:
             raise ValueError("block_table is a contiguous int32 [batch, stride] CUDA tensor "
                              "beside the pools")
         n_blocks, stride = int(prefix[0].shape[0]), int(block_table.shape[1])
-        held.append(block_table)
     ptrs = [_ptr(t) if t is not None and t.numel() else None
             for part in (prefix, ring) for t in (part or (None,) * 3)]
     cache = PsKVCacheQ4(*ptrs, int(batch), _ptr(block_table), n_blocks, stride, 0)
     cache.held = held  # the struct keeps only addresses
     cache.device = held[0].get_device() if held else None
+    # what _store_q4_fits compares with a call's geometry
+    cache.rows = tuple(tuple(part[0].shape[:-1]) if part is not None and part[0].numel() else None
+                       for part in (prefix, ring))
+    cache.table_rows = None if block_table is None else int(block_table.shape[0])
+    cache.fits = None
     return cache
+
+
+def _store_q4_fits(params: PsParams, cache: PsKVCacheQ4) -> None:
+    """Refuses a 4-bit store (of make_cache_q4) whose tensors are not those of the call's geometry:
+    the kernels index by that alone."""
+    hkv, lp, w, batch = params.n_kv_heads, params.l_prefix, params.window, cache.batch
+    fits = getattr(cache, "fits", ())
+    if fits == (hkv, lp, w, batch) or fits == ():  # seen before; or filled by hand, addresses alone
+        return
+    prefix, ring = cache.rows
+
+    def holds(shape, rows):
+        return len(shape) == 3 and shape[0] >= batch and shape[1:] == (hkv, rows)
+    if cache.table_rows is not None:
+        ok = cache.table_rows >= batch and (prefix is None or prefix[1:] == (hkv, 64))
+    else:
+        ok = (prefix is None or lp == 0 or holds(prefix, lp)) and (ring is None or holds(ring, w))
+    if not ok:
+        raise ValueError(f"a 4-bit store of prefix rows {prefix} and ring rows {ring} ([batch, Hkv, "
+                         f"rows], pools [blocks, Hkv, 64]) does not hold batch {batch}, Hkv {hkv}, "
+                         f"l_prefix {lp}, window {w}")
+    cache.fits = (hkv, lp, w, batch)
+
+
+def _store_fits(params: PsParams, cache: PsKVCache, device: int) -> None:
+    """The same for a bf16 store of make_cache."""
+    hkv, lp, w, batch = params.n_kv_heads, params.l_prefix, params.window, cache.batch
+    held = getattr(cache, "held", None)
+    if held is None or getattr(cache, "fits", None) == (hkv, lp, w, batch, device):
+        return
+    for t, rows in zip(held, (lp, lp, w, w)):
+        if t is not None and rows and t.numel():
+            shape = tuple(t.shape)
+            if t.dtype is not _torch().bfloat16 or t.get_device() != device or \
+                    not t.is_contiguous() or t.numel() < batch * hkv * rows * 128 or \
+                    (len(shape) == 4 and shape[1:] != (hkv, rows, 128)):
+                raise ValueError(f"a store part of batch {batch} is contiguous bf16 [batch, {hkv}, "
+                                 f"{rows}, 128] on cuda:{device}, got {t.dtype} {shape} on "
+                                 f"{t.device}")
+    cache.fits = (hkv, lp, w, batch, device)
 
 
 # ---------------------------------------------------------------- entry points
@@ -657,6 +708,7 @@ def ps_kv_append_norm_rope(params: PsParams, rope: PsRope, norm, cache: PsKVCach
                            q, q_out, pos0, T: int, dev_status=None, stream=None) -> None:
     """ps_kv_append_rope with a head norm and any rotary plan; q (or None) goes to q_out."""
     dev = _device_of(pos0, norm)
+    _store_fits(params, cache, dev)
     rc = load().ps_kv_append_norm_rope(params, rope, norm, cache,
                                        *_append_rows(params, cache.batch, k_new, v_new, q, q_out,
                                                      pos0, T, dev),
@@ -687,6 +739,7 @@ def ps_kv_append_norm_rope_q4(params: PsParams, rope: PsRope, norm, cache: PsKVC
                               stream=None) -> None:
     """The same into a 4-bit store (make_cache_q4)."""
     dev = _device_of(pos0, norm, cache)
+    _store_q4_fits(params, cache)
     rc = load().ps_kv_append_norm_rope_q4(params, rope, norm, cache,
                                           *_append_rows(params, cache.batch, k_new, v_new, q,
                                                         q_out, pos0, T, dev),
@@ -699,6 +752,7 @@ def ps_kv_read_q4(params: PsParams, cache: PsKVCacheQ4, pos0, T: int, k_out, v_o
     """Rows of positions [pos0, pos0 + T) of a 4-bit store as bf16 [batch, T, Hkv, 128]."""
     torch = _torch()
     dev = _device_of(pos0, None, cache)
+    _store_q4_fits(params, cache)
     n = cache.batch * int(T) * params.n_kv_heads * 128
     out = [None if t is None else _tensor(name, t, torch.bfloat16, dev, n)
            for name, t in (("k_out", k_out), ("v_out", v_out))]
@@ -716,6 +770,7 @@ def ps_decode_attn_q4(params: PsParams, cache: PsKVCacheQ4, q, pos, out, lse=Non
     """ps_decode_attn over a 4-bit store."""
     torch = _torch()
     dev = _device_of(pos, None, cache)
+    _store_q4_fits(params, cache)
     rows = cache.batch * params.n_q_heads
     ws, ws_bytes = _workspace(workspace, dev)
     rc = load().ps_decode_attn_q4(
