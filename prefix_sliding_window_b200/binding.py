@@ -560,6 +560,12 @@ def _tensor(name: str, t, dtype, device: int, numel: int):
     return t.data_ptr()
 
 
+def _pair(name: str, given, out) -> None:
+    """Both of them are tensors, or both None: one alone would be left unwritten or unread."""
+    if (given is None) != (out is None):
+        raise ValueError(f"{name} go together")
+
+
 def _heads(name: str, t, tokens: int, heads: int, device: int):
     """Rows of heads: [tokens, heads, 128] (or leading dims that flatten to tokens) with heads
     contiguous in a token.  Returns the address and the stride between tokens."""
@@ -639,6 +645,8 @@ def ps_qk_norm_rope(params: PsParams, rope: PsRope, norm, q, k, pos, q_out, k_ou
     """Head norm (norm None: none) and rotation of q [N, Hq, 128] and k [N, Hkv, 128] (views of
     packed rows allowed; either None with its output) at pos [N]."""
     torch = _torch()
+    _pair("q and q_out", q, q_out)
+    _pair("k and k_out", k, k_out)
     dev = _device_of(pos, norm)
     n = pos.numel()
     hq, hkv = params.n_q_heads, params.n_kv_heads
@@ -666,6 +674,8 @@ def ps_qk_norm_rope_bwd(params: PsParams, rope: PsRope, norm, q, k, pos, dq_out,
     """Gradients of ps_qk_norm_rope: dq, dk (views of packed rows allowed) and, where given, the
     weights' (fp32 [128])."""
     torch = _torch()
+    _pair("dq_out and dq", dq_out, dq)
+    _pair("dk_out and dk", dk_out, dk)
     dev = _device_of(pos, norm)
     n = pos.numel()
     hq, hkv = params.n_q_heads, params.n_kv_heads
@@ -693,6 +703,7 @@ def ps_qk_norm_rope_bwd(params: PsParams, rope: PsRope, norm, q, k, pos, dq_out,
 
 def _append_rows(params, batch, k_new, v_new, q, q_out, pos0, T, dev):
     torch = _torch()
+    _pair("q and q_out", q, q_out)
     n = int(batch) * int(T)
     kp, ks = _heads("k_new", k_new, n, params.n_kv_heads, dev)
     vp, vs = _heads("v_new", v_new, n, params.n_kv_heads, dev)

@@ -148,3 +148,22 @@ def test_bf16_stores():
                  (part(*pre), part(*pre, device=1), part(*ring), part(*ring), 4)):
         with pytest.raises(ValueError):
             B._store_fits(p, B.make_cache(*args), 0)
+
+
+def test_one_of_a_pair_refused():
+    """An input without its output, or the other way round: left out without a word it would leave
+    an output unwritten."""
+    p = B.make_params(4, 2, 128, 100, 512)
+    rope = B.make_rope(p)
+    q, k = (torch.zeros(3, h, 128, dtype=torch.bfloat16) for h in (4, 2))
+    pos = torch.zeros(3, dtype=torch.int64)
+    for args in ((None, k, pos, q, k), (q, k, pos, None, k), (q, None, pos, q, k),
+                 (q, k, pos, q, None)):
+        with pytest.raises(ValueError, match="go together"):
+            B.ps_qk_norm_rope(p, rope, None, *args)
+    for args in ((None, k, q, k), (q, k, None, k), (q, None, q, k), (q, k, q, None)):
+        with pytest.raises(ValueError, match="go together"):
+            B.ps_qk_norm_rope_bwd(p, rope, None, q, k, pos, *args)
+    for args in ((None, q), (q, None)):
+        with pytest.raises(ValueError, match="go together"):
+            B._append_rows(p, 3, k, k, *args, pos, 1, 0)
