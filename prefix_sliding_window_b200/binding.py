@@ -68,6 +68,8 @@ class PsKVCache(ctypes.Structure):
         ("v_ring", c_void_p),
         ("batch", c_int64),
     ]
+    held = None  # make_cache's tensors; None: addresses alone
+    fits = None  # the geometry they were last compared with
 
 
 class PsRope(ctypes.Structure):
@@ -98,6 +100,7 @@ class PsQkNorm(ctypes.Structure):
         ("weight_type", c_int32),
         ("eps", c_float),
     ]
+    device = None  # of make_norm's weights; None: not known
 
 
 class PsKVCacheQ4(ctypes.Structure):
@@ -114,6 +117,9 @@ class PsKVCacheQ4(ctypes.Structure):
         ("table_stride", c_int32),
         ("reserved", c_int32),
     ]
+    device = None  # of make_cache_q4's tensors; None: not known
+    rows = None    # their (prefix, ring) rows; None: addresses alone
+    fits = None    # the geometry they were last compared with
 
 
 _lib = None
@@ -330,16 +336,14 @@ def make_cache_q4(prefix, ring, batch: int, block_table=None) -> PsKVCacheQ4:
     cache.rows = tuple(tuple(part[0].shape[:-1]) if part is not None and part[0].numel() else None
                        for part in (prefix, ring))
     cache.table_rows = None if block_table is None else int(block_table.shape[0])
-    cache.fits = None
     return cache
 
 
 def _store_q4_fits(params: PsParams, cache: PsKVCacheQ4) -> None:
     """Refuses a 4-bit store (of make_cache_q4) whose tensors are not those of the call's geometry:
     the kernels index by that alone."""
-    hkv, lp, w, batch = params.n_kv_heads, params.l_prefix, params.window, cache.batch
-    fits = getattr(cache, "fits", ())
-    if fits == (hkv, lp, w, batch) or fits == ():  # seen before; or filled by hand, addresses alone
+    geometry = hkv, lp, w, batch = (params.n_kv_heads, params.l_prefix, params.window, cache.batch)
+    if cache.fits == geometry or cache.rows is None:
         return
     prefix, ring = cache.rows
 
@@ -353,16 +357,16 @@ def _store_q4_fits(params: PsParams, cache: PsKVCacheQ4) -> None:
         raise ValueError(f"a 4-bit store of prefix rows {prefix} and ring rows {ring} ([batch, Hkv, "
                          f"rows], pools [blocks, Hkv, 64]) does not hold batch {batch}, Hkv {hkv}, "
                          f"l_prefix {lp}, window {w}")
-    cache.fits = (hkv, lp, w, batch)
+    cache.fits = geometry
 
 
 def _store_fits(params: PsParams, cache: PsKVCache, device: int) -> None:
     """The same for a bf16 store of make_cache."""
-    hkv, lp, w, batch = params.n_kv_heads, params.l_prefix, params.window, cache.batch
-    held = getattr(cache, "held", None)
-    if held is None or getattr(cache, "fits", None) == (hkv, lp, w, batch, device):
+    hkv, lp, w, batch, _ = geometry = (params.n_kv_heads, params.l_prefix, params.window,
+                                       cache.batch, device)
+    if cache.fits == geometry or cache.held is None:
         return
-    for t, rows in zip(held, (lp, lp, w, w)):
+    for t, rows in zip(cache.held, (lp, lp, w, w)):
         if t is not None and rows and t.numel():
             shape = tuple(t.shape)
             if t.dtype is not _torch().bfloat16 or t.get_device() != device or \
@@ -371,7 +375,7 @@ def _store_fits(params: PsParams, cache: PsKVCache, device: int) -> None:
                 raise ValueError(f"a store part of batch {batch} is contiguous bf16 [batch, {hkv}, "
                                  f"{rows}, 128] on cuda:{device}, got {t.dtype} {shape} on "
                                  f"{t.device}")
-    cache.fits = (hkv, lp, w, batch, device)
+    cache.fits = geometry
 
 
 # ---------------------------------------------------------------- entry points
@@ -616,9 +620,10 @@ def _device_of(pos, norm=None, cache=None) -> int:
     if dev < 0 or dev != _current_device():
         raise ValueError(f"positions are on {pos.device}, the current device is "
                          f"cuda:{_torch().cuda.current_device()}")
-    for what in (norm, cache):
-        if what is not None and getattr(what, "device", None) not in (None, dev):
-            raise ValueError(f"weights or cache on cuda:{what.device}, positions on cuda:{dev}")
+    if norm is not None and norm.device != dev and norm.device is not None:
+        raise ValueError(f"weights on cuda:{norm.device}, positions on cuda:{dev}")
+    if cache is not None and cache.device != dev and cache.device is not None:
+        raise ValueError(f"cache on cuda:{cache.device}, positions on cuda:{dev}")
     return dev
 
 
