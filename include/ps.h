@@ -202,7 +202,9 @@ int ps_qk_norm_rope_bwd(const ps_params* params, const ps_rope* rope, const ps_q
  * are normalised, rotated at pos0[b] + t and stored, values stored as they are, queries
  * normalised and rotated into q_out.  Where a token's row goes, and which tokens are skipped
  * (their q_out rows are zeros), is as ps_kv_append_rope; in addition a position >= 2^31 is
- * skipped (PS_DEV_POS_RANGE).
+ * skipped (PS_DEV_POS_RANGE).  Without a norm and with a plain rope, the rows are those of
+ * ps_kv_append_rope but for a rounding of few (35 elements in a million: the two round cosines and
+ * sines differently), so that one call may continue what the other began.
  *   k_new, v_new : device bf16, token (b, t) at k_new + (b * T + t) * k_stride, [Hkv, D].
  *   q            : device bf16, token (b, t) at q + (b * T + t) * q_stride, [Hq, D], or NULL
  *                  together with q_out.

@@ -354,9 +354,9 @@ def _store_q4_fits(params: PsParams, cache: PsKVCacheQ4) -> None:
     else:
         ok = (prefix is None or lp == 0 or holds(prefix, lp)) and (ring is None or holds(ring, w))
     if not ok:
-        raise ValueError(f"a 4-bit store of prefix rows {prefix} and ring rows {ring} ([batch, Hkv, "
-                         f"rows], pools [blocks, Hkv, 64]) does not hold batch {batch}, Hkv {hkv}, "
-                         f"l_prefix {lp}, window {w}")
+        raise ValueError(f"a 4-bit store of prefix rows {prefix} and ring rows {ring} ([batch, "
+                         f"Hkv, rows], pools [blocks, Hkv, 64]) does not hold batch {batch}, Hkv "
+                         f"{hkv}, l_prefix {lp}, window {w}")
     cache.fits = geometry
 
 

@@ -4,9 +4,9 @@
 // One pass: a token's packed q, k and v heads are read once; keys are normalised, rotated at the
 // token's position and written to their prefix row or ring slot, values go straight there, queries
 // to q_out.  Bound by HBM and issue slots for long prompts (4 x 8192 tokens of 28 + 4 heads, half
-// of them kept: 97 us, 86 % of a copy's rate; into 4 bits 115 us) and by latency for a decode
-// step's single tokens.  Of tokens that share a ring slot only the newest of the call is written,
-// so the result does not depend on which block runs first.
+// of them kept, back to back in a graph: 97 us, 86 % of a copy's rate; into 4 bits 115 us) and by
+// latency for a decode step's single tokens.  Of tokens that share a ring slot only the newest of
+// the call is written, so the result does not depend on which block runs first.
 //
 // A warp keeps a token's angles and weights in registers over all of its heads, as in the pass
 // without a store; with few tokens eight warps share one.

@@ -33,12 +33,12 @@
 // instructions a tile in setting up their uniform operands, a fifth of all; tiles of 256 rows for
 // the whole block amortised that, but had to land whole before any warp could start.)
 //
-// Measured, 28 / 4 heads or 16 / 2: 296 units of 32768 rows 218 us, as fast as a copy of the same
-// bytes; 1024 of 4196 rows 110 us (5.6 TB/s), 128 of them 21 us (one block an SM, whose loads
-// saturate at 46 GB/s), 8 of 131072 rows 34 us, 2 of 612 rows 6.8 us.  Equal shares of all rows for
-// one wave of blocks, whatever units they span, balance better on paper, but finding a share took
-// 5 us of scanning positions, each border a start, an end and a merge, and the SMs do not run
-// equally fast: 134 us for the 1024, 49 us where 280 units take 35 one by one.
+// Measured back to back in a graph, 28 / 4 heads or 16 / 2: 296 units of 32768 rows 220 us, as fast
+// as a copy of the same bytes; 1024 of 4196 rows 110 us (5.6 TB/s), 128 of them 21 us (12 us at a
+// copy's rate, the rest start and end), 8 of 131072 rows 34 us, 2 of 612 rows 7.3 us.  Equal shares
+// of all rows for one wave of blocks, whatever units they span, balance better on paper, but
+// finding a share took 5 us of scanning positions, each border a start, an end and a merge, and the
+// SMs do not run equally fast: 134 us for the 1024, 49 us where 280 units take 35 one by one.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -759,10 +759,11 @@ __global__ void __launch_bounds__(kMaxGroup * 32) merge_q4_kernel(const DecodeQ4
 // In how many blocks a unit is worked on, at most.  Pieces fill the SMs and even out the last wave
 // of blocks, but each starts and ends on its own and has to be merged.  Of the numbers that fill
 // one to eight halves of a wave, the one of least time is taken, with 0.1 us for a tile of each of
-// an SM's two blocks (46 GB/s an SM), 4 us for a block's start and end and 2 us for a merge.  Half a
-// wave of pieces counts as a whole one: behind another kernel some SMs get two of its blocks (74
-// units of 4196 rows: 21.4 us in two pieces, 16.0 in four).  Whole units: 40 of 32768 rows take
-// 110.9 us in one piece, 77.3 in seven; 1024 of 8448 rows 200 in one, 218 in two.
+// an SM's two blocks (46 GB/s an SM: HBM's rate over all of them), 4 us for a block's start and end
+// and 2 us for a merge.  Half a wave of pieces counts as a whole one: behind another kernel some
+// SMs get two of its blocks (74 units of 4196 rows: 21.4 us in two pieces, 16.0 in four).  Whole
+// units: 40 of 32768 rows take 110.9 us in one piece, 77.3 in seven; 1024 of 8448 rows 200 in one,
+// 218 in two.
 int64_t plan_decode(int64_t batch, int32_t hkv, int64_t max_keys) {
   const int64_t units = batch * hkv, sms = sm_count();
   const int64_t tiles = max_keys / kTile + 3;  // (a partial one at the end of each run)

@@ -158,11 +158,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // reduced modulo 2 pi there, with 2 pi split in two parts (Cody-Waite: the first has 24
 // significant bits, so k * part1 is exact for |k| < 2^29; the second carries the rest in
 // double precision); the remainder, within [-pi, pi], goes through fp32 sincosf (accurate to
-// ~1e-7 there).  At p ~ 2^18 an fp32 product alone would be off by ~0.03 rad.  Every kernel
-// that rotates keys or queries uses this function and rope_lo / rope_hi, so a vector rotated
-// by any of them is bit-identical.  Out of line: sincosf carries a large slow path (for
-// arguments it never gets here), which would otherwise sit inside the callers' hot loops.
-// Returns (cos, sin).
+// ~1e-7 there).  At p ~ 2^18 an fp32 product alone would be off by ~0.03 rad.  The plain append
+// (alone and in the fused step) and Reset PE's second rotation use this function and rope_lo /
+// rope_hi, so a vector rotated by any of them is bit-identical.  The norm + rotary pass and the
+// appends with it form theirs by cos_sin_of (ps_norm_rope.cuh): without a norm, 35 in a million of
+// their bf16 results differ from the plain append's by a rounding.  Out of line: sincosf carries a
+// large slow path (for arguments it never gets here), which would otherwise sit inside the callers'
+// hot loops.  Returns (cos, sin).
 static __device__ __noinline__ float2 rope_cos_sin(double p, double inv_f) {
   const double ang = p * inv_f;
   const double k = rint(ang * 0.15915494309189535);

@@ -9,8 +9,9 @@
 // prefetch costs no registers (two items ahead in registers: 132 us forward at 4 x 8192 tokens of
 // 28 + 4 heads, 106 with the ring).  With few tokens eight warps share one.
 //
-// At 4 x 8192 tokens of 28 + 4 heads the forward takes 86 us (6.3 TB/s, 97 % of a copy's rate), the
-// backward 132 us (94 %).  Three blocks of 80 registers an SM: 97 and more.
+// At 4 x 8192 tokens of 28 + 4 heads, back to back in a graph, the forward takes 86 us (6.2 TB/s,
+// 96 % of a copy's rate), the backward 132 us (94 %); a call between others, which finds their
+// lines in L2, 93 and 148.  Three blocks of 80 registers an SM: 97 and more.
 #include <cuda_bf16.h>
 
 #include "ps_norm_rope.cuh"

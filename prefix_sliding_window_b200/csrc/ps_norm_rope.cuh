@@ -110,9 +110,9 @@ __device__ __forceinline__ void pack_pairs(const uint64_t (&u)[4], const uint64_
 // difference is exact, so the remainder is good to 2^-53 of pi/2 beside the product's own
 // rounding), then Taylor sums, off by 2e-10 (cos, to r^10) and 2e-9 (sin, to r^9): what is added to
 // the first terms in fp32, the sum in float64, so that nearly all results are the correctly rounded
-// ones.  40 instructions where the library's other rotations, through sincosf, take 240: with
-// 16 + 2 heads a token's 64 angles were a fifth of the forward's time (73 us at 32768 tokens, 64
-// with these).
+// ones.  About 30 operations where the library's other rotations, through sincosf, take 240
+// instructions: with 16 + 2 heads a token's 64 angles were a fifth of the forward's time (73 us at
+// 32768 tokens, 64 with these).
 __device__ __forceinline__ float2 cos_sin_of(double p, double inv_f) {
   const double ang = p * inv_f;
   const double shifter = 6755399441055744.0;  // 1.5 2^52: the sum's low word holds the integer
@@ -218,8 +218,9 @@ __device__ __forceinline__ float row_rstd(const uint64_t (&u)[4], const uint64_t
   return rsqrtf(row_sum(x.x + x.y) * (1.f / kHeadDim) + eps);
 }
 
-// The same, with the squares summed four neighbours in turn, then halves onto halves (where
-// p.halves): the order of a plain evaluation's sum.
+// The same, with the squares summed four neighbours in turn, then halves onto halves: the order of
+// a plain evaluation's sum.  Only where every lane's chunks are eight apart (p.halves: interleaved
+// pairs, or heads rotated whole); half pairs of a part of the head take the other order.
 template <bool INTER>
 __device__ __forceinline__ float row_rstd_by_halves(const uint64_t (&u)[4], const uint64_t (&v)[4],
                                                     float eps) {
