@@ -286,10 +286,10 @@ size_t ps_decode_q4_workspace_bytes(const ps_params* params, int64_t batch);
  * and that block's rows are left out.  Positions reach 2^31 - 1, as the append's
  * (PS_DEV_POS_RANGE above).  Queries have to be below 2^79 in magnitude, values below 2^90 and
  * softmax_scale at most 2^32 (PS_ERR_UNSUPPORTED); values may differ by any factor from row to row
- * and between the groups of a row.  A visible group that stands for NaN makes what it reaches NaN:
- * of K its head's outputs and lse, of V that group's dims.  Other arguments, results and errors as
- * ps_decode_attn; the workspace is ps_decode_q4_workspace_bytes(), 16-byte aligned, and of one call
- * at a time. */
+ * and between the groups of a row (a weight below 2^-126 of the greatest counts as none).  A
+ * visible group that stands for NaN makes what it reaches NaN: of K its head's outputs and lse, of
+ * V that group's dims.  Other arguments, results and errors as ps_decode_attn; the workspace is
+ * ps_decode_q4_workspace_bytes(), 16-byte aligned, and of one call at a time. */
 int ps_decode_attn_q4(const ps_params* params, const ps_kv_cache_q4* cache, const void* q,
                       const int64_t* pos, void* out, float* lse, void* workspace,
                       size_t ws_bytes, int32_t* dev_status, ps_stream_t stream);

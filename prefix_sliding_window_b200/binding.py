@@ -8,6 +8,7 @@ the library's CUDA kernels; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
@@ -347,10 +348,14 @@ def _store_q4_fits(params: PsParams, cache: PsKVCacheQ4) -> None:
         return
     prefix, ring = cache.rows
 
-    def holds(shape, rows):
-        return len(shape) == 3 and shape[0] >= batch and shape[1:] == (hkv, rows)
+    def holds(shape, rows):  # [batch, Hkv, rows], or rows in other dims if there are enough
+        if len(shape) == 3:
+            return shape[0] >= batch and shape[1:] == (hkv, rows)
+        return math.prod(shape) >= batch * hkv * rows
     if cache.table_rows is not None:
-        ok = cache.table_rows >= batch and (prefix is None or prefix[1:] == (hkv, 64))
+        ok = cache.table_rows >= batch and (prefix is None or prefix[1:] == (hkv, 64)
+                                            or len(prefix) != 3
+                                            and math.prod(prefix[1:]) >= hkv * 64)
     else:
         ok = (prefix is None or lp == 0 or holds(prefix, lp)) and (ring is None or holds(ring, w))
     if not ok:

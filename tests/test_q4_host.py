@@ -67,6 +67,7 @@ PREFIX, RING = (4, 2, 100), (4, 2, 512)
     (PREFIX, RING, 4, (2, 0, 512)),            # no prefix row is asked for
     (PREFIX, None, 4, (2, 100, 1)),            # linear
     ((4, 2, 0), RING, 4, (2, 0, 512)),
+    ((8, 100), RING, 4, (2, 100, 512)),        # the same rows without the batch's dim
 ])
 def test_stores_that_hold_the_geometry(prefix, ring, batch, geometry):
     cache = B.make_cache_q4(prefix and _part(*prefix), ring and _part(*ring), batch)
@@ -85,7 +86,7 @@ def test_stores_that_hold_the_geometry(prefix, ring, batch, geometry):
     (PREFIX, RING, 4, (2, 100, 256)),
     (PREFIX, (2, 2, 512), 4, (2, 100, 512)),   # the ring of another batch
     (PREFIX, None, 4, (2, 128, 1)),
-    ((8, 100), RING, 4, (2, 100, 512)),        # rows without a batch
+    ((8, 99), RING, 4, (2, 100, 512)),
 ])
 def test_stores_that_do_not(prefix, ring, batch, geometry):
     cache = B.make_cache_q4(prefix and _part(*prefix), ring and _part(*ring), batch)
