@@ -276,7 +276,8 @@ int ps_kv_read_q4(const ps_params* params, const ps_kv_cache_q4* cache, const in
                   int32_t T, void* k_out, void* v_out, int32_t* dev_status, ps_stream_t stream);
 
 /* Bytes of device workspace ps_decode_attn_q4 needs for this geometry and batch (any store
- * kind; for a linear store l_prefix = Lmax).  0 on invalid arguments. */
+ * kind; for a linear store l_prefix = Lmax).  0 where none is needed (the workspace may then be
+ * NULL) and on invalid arguments. */
 size_t ps_decode_q4_workspace_bytes(const ps_params* params, int64_t batch);
 
 /* ps_decode_attn over the 4-bit store: attention of one query token per sequence over the
